@@ -6,5 +6,7 @@ device memory and streams.
 """
 
 from . import abi  # noqa: F401
-from .abi import (moe_combine, moe_dispatch, moe_grouped_ffn, moe_layer_forward,  # noqa: F401
-                  moe_read_device_flags, moe_route_topk, moe_workspace_size, make_shape)
+from .abi import (make_block, make_shape, moe_block_forward, moe_block_forward_int8, moe_combine,  # noqa: F401
+                  moe_combine_norm, moe_dispatch, moe_grouped_ffn, moe_grouped_ffn_int8, moe_grouped_gemm_int8,
+                  moe_layer_forward, moe_norm, moe_quantize_int8, moe_read_device_flags, moe_route_biased,
+                  moe_route_topk, moe_workspace_size)

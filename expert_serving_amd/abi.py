@@ -24,7 +24,10 @@ EXPORTED = ("moe_workspace_size", "moe_route_topk", "moe_dispatch", "moe_map_rep
             "moe_combine", "moe_layer_forward", "moe_group_score_sigmoid", "moe_status_string",
             "moe_last_hip_error", "moe_read_device_flags", "moe_quantize_mxfp8", "moe_workspace_size_mxfp8",
             "moe_grouped_ffn_mxfp8", "moe_layer_forward_mxfp8", "moe_layer_forward_noalloc",
-            "moe_ep_dispatch_layout", "moe_ep_combine", "moe_convert_bf16_to_f16")
+            "moe_ep_dispatch_layout", "moe_ep_combine", "moe_convert_bf16_to_f16", "moe_route_biased",
+            "moe_quantize_int8", "moe_workspace_size_gemm_int8", "moe_grouped_gemm_int8", "moe_workspace_size_int8",
+            "moe_grouped_ffn_int8", "moe_norm", "moe_combine_norm", "moe_workspace_size_block", "moe_block_forward",
+            "moe_block_forward_int8")
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -57,6 +60,22 @@ class MoeMxfp8Ffn(ctypes.Structure):
     _fields_ = [("gate", ctypes.c_void_p), ("gate_scales", ctypes.c_void_p),
                 ("up", ctypes.c_void_p), ("up_scales", ctypes.c_void_p),
                 ("down", ctypes.c_void_p), ("down_scales", ctypes.c_void_p)]
+
+
+class MoeInt8Ffn(ctypes.Structure):
+    """moe_int8_ffn: int8 codes and per-channel scales of the gate, up and down weights."""
+    _fields_ = [("gate", ctypes.c_void_p), ("gate_scales", ctypes.c_void_p),
+                ("up", ctypes.c_void_p), ("up_scales", ctypes.c_void_p),
+                ("down", ctypes.c_void_p), ("down_scales", ctypes.c_void_p)]
+
+
+class MoeBlock(ctypes.Structure):
+    """moe_block: the norms, gate, residual scale and balance bias of the block around a layer.
+    make_block keeps the tensors it points into."""
+    _fields_ = [("select_bias", ctypes.c_void_p), ("pre_norm", ctypes.c_void_p), ("post_norm", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float), ("gate", ctypes.c_void_p),
+                ("gate_row_stride", ctypes.c_int64), ("gate_col_stride", ctypes.c_int32),
+                ("gate_dtype", ctypes.c_int32), ("stream_dtype", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -103,6 +122,19 @@ def lib():
         L.moe_grouped_ffn_mxfp8.argtypes = [sp, vp, vp, i32, vp, mp, vp, vp, sz, vp]
         L.moe_layer_forward_mxfp8.argtypes = [sp, vp, vp, vp, vp, mp, mp, vp, ctypes.POINTER(MoeDebug), vp,
                                               sz, vp]
+        bp, fp = ctypes.POINTER(MoeBlock), ctypes.POINTER(MoeInt8Ffn)
+        szp = ctypes.POINTER(ctypes.c_size_t)
+        L.moe_route_biased.argtypes = [sp] + [vp] * 10 + [sz, vp]
+        L.moe_quantize_int8.argtypes = [i32, i32, i32, vp, vp, vp, vp]
+        L.moe_workspace_size_gemm_int8.argtypes = [i32, i32, i32, i32, szp]
+        L.moe_grouped_gemm_int8.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]
+        L.moe_workspace_size_int8.argtypes = [sp, szp]
+        L.moe_grouped_ffn_int8.argtypes = [sp, vp, vp, vp, fp, i32, vp, vp, sz, vp]
+        L.moe_norm.argtypes = [i32, i32, i32, vp, vp, ctypes.c_float, i32, vp, vp, vp, vp]
+        L.moe_combine_norm.argtypes = [sp, bp, i32, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_workspace_size_block.argtypes = [sp, szp]
+        L.moe_block_forward.argtypes = [sp, bp] + [vp] * 11 + [ctypes.POINTER(MoeDebug), vp, sz, vp]
+        L.moe_block_forward_int8.argtypes = [sp, bp, vp, vp, vp, vp, fp, fp, vp, ctypes.POINTER(MoeDebug), vp, sz, vp]
         for name in EXPORTED:
             if name not in ("moe_status_string", "moe_last_hip_error"):
                 getattr(L, name).restype = st
@@ -332,3 +364,126 @@ def moe_layer_forward_mxfp8(shape, x, w_router, router_bias, k_per_token, expert
                                          ctypes.byref(d) if d is not None else None, _ptr(ws),
                                          ws.numel() if ws_bytes is None else ws_bytes, _stream(stream)),
            "moe_layer_forward_mxfp8")
+
+
+# ---- routing with a balance bias, int8 experts, the block around the layer ---------
+
+def moe_route_biased(shape, x, w_router, router_bias, select_bias, logits_in, logits_out, k_per_token, topk_ids,
+                     topk_gates, ws, ws_bytes=None, stream=None):
+    _check(lib().moe_route_biased(ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(router_bias), _ptr(select_bias),
+                                  _ptr(logits_in), _ptr(logits_out), _ptr(k_per_token), _ptr(topk_ids),
+                                  _ptr(topk_gates), _ptr(ws), ws.numel() if ws_bytes is None else ws_bytes,
+                                  _stream(stream)), "moe_route_biased")
+
+
+def moe_quantize_int8(rows, cols, src_dtype, src, codes, scales, stream=None):
+    _check(lib().moe_quantize_int8(int(rows), int(cols), int(src_dtype), _ptr(src), _ptr(codes), _ptr(scales),
+                                   _stream(stream)), "moe_quantize_int8")
+
+
+def quantize_int8(t, stream=None):
+    """(codes int8 of t's shape, scales fp32 of its leading dimensions) of a bf16, fp32 or fp16 device tensor."""
+    import torch
+    dt = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}[t.dtype]
+    codes = torch.empty(t.shape, dtype=torch.int8, device=t.device)
+    scales = torch.empty(t.shape[:-1], dtype=torch.float32, device=t.device)
+    moe_quantize_int8(scales.numel(), t.shape[-1], dt, t.contiguous(), codes, scales, stream)
+    return codes, scales
+
+
+def int8_ffn(gate, up, down):
+    """One FFN's int8 weights from (codes, scales) pairs (routed [E][I][H] / [E][H][I] with scales [E][I] /
+    [E][H], or shared [Is][H] / [H][Is]): a dict of the device tensors plus the struct under "abi"."""
+    st = MoeInt8Ffn(*(_ptr(t) for pair in (gate, up, down) for t in pair))
+    return dict(gate=gate, up=up, down=down, abi=st)
+
+
+def moe_workspace_size_gemm_int8(rows, n, k, num_experts) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().moe_workspace_size_gemm_int8(int(rows), int(n), int(k), int(num_experts), ctypes.byref(b)),
+           "moe_workspace_size_gemm_int8")
+    return int(b.value)
+
+
+def moe_grouped_gemm_int8(rows, n, k, num_experts, a, a_scales, expert_offsets, b, b_scales, y_dtype, y, ws,
+                          ws_bytes=None, stream=None):
+    _check(lib().moe_grouped_gemm_int8(int(rows), int(n), int(k), int(num_experts), _ptr(a), _ptr(a_scales),
+                                       _ptr(expert_offsets), _ptr(b), _ptr(b_scales), int(y_dtype), _ptr(y),
+                                       _ptr(ws), ws.numel() if ws_bytes is None else ws_bytes, _stream(stream)),
+           "moe_grouped_gemm_int8")
+
+
+def moe_workspace_size_int8(shape: MoeShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_workspace_size_int8(ctypes.byref(shape), ctypes.byref(n)), "moe_workspace_size_int8")
+    return int(n.value)
+
+
+def moe_grouped_ffn_int8(shape, x_codes, x_scales, expert_offsets, experts, y_dtype, y_perm, ws, ws_bytes=None,
+                         stream=None):
+    _check(lib().moe_grouped_ffn_int8(ctypes.byref(shape), _ptr(x_codes), _ptr(x_scales), _ptr(expert_offsets),
+                                      _mx(experts), int(y_dtype), _ptr(y_perm), _ptr(ws),
+                                      ws.numel() if ws_bytes is None else ws_bytes, _stream(stream)),
+           "moe_grouped_ffn_int8")
+
+
+def moe_norm(rows, cols, src_dtype, x, weight, eps, out_dtype, out, codes, scales, stream=None):
+    _check(lib().moe_norm(int(rows), int(cols), int(src_dtype), _ptr(x), _ptr(weight), float(eps), int(out_dtype),
+                          _ptr(out), _ptr(codes), _ptr(scales), _stream(stream)), "moe_norm")
+
+
+def make_block(select_bias=None, pre_norm=None, post_norm=None, eps=1e-6, gate=None, residual_scale=1.0,
+               stream_dtype=MOE_BF16) -> MoeBlock:
+    """A moe_block from device tensors.  gate: a bf16 or fp32 tensor that broadcasts to [T, H] -- [H] or [1, H]
+    (a value per channel), [T, 1] (a value per token) or [T, H], rows at any stride, columns one apart."""
+    b = MoeBlock(_ptr(select_bias), _ptr(pre_norm), _ptr(post_norm), float(eps), float(residual_scale), _ptr(gate),
+                 0, 0, MOE_F32, int(stream_dtype))
+    if gate is not None:
+        import torch
+        rows, cols = gate.shape if gate.dim() == 2 else (1, gate.shape[0])
+        if cols > 1 and gate.stride(-1) not in (0, 1):
+            raise ValueError("the gate's columns have to be one element apart")
+        b.gate_row_stride = gate.stride(0) if rows > 1 else 0
+        b.gate_col_stride = gate.stride(-1) if cols > 1 else 0
+        b.gate_dtype = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}[gate.dtype]
+    b.tensors = (select_bias, pre_norm, post_norm, gate)
+    return b
+
+
+def moe_combine_norm(shape, block, y_dtype, y_perm, row_of_slot, topk_gates, y_shared, residual, out, stream=None):
+    _check(lib().moe_combine_norm(ctypes.byref(shape), ctypes.byref(block), int(y_dtype), _ptr(y_perm),
+                                  _ptr(row_of_slot), _ptr(topk_gates), _ptr(y_shared), _ptr(residual), _ptr(out),
+                                  _stream(stream)), "moe_combine_norm")
+
+
+def moe_workspace_size_block(shape: MoeShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_workspace_size_block(ctypes.byref(shape), ctypes.byref(n)), "moe_workspace_size_block")
+    return int(n.value)
+
+
+def _dbg(dbg):
+    if dbg is None or isinstance(dbg, MoeDebug):
+        return dbg
+    return MoeDebug(**{k: _ptr(v) for k, v in dbg.items()}) if dbg else None
+
+
+def moe_block_forward(shape, block, x, w_router, router_bias, k_per_token, w_gate, w_up, w_down, ws_gate, ws_up,
+                      ws_down, out, dbg, ws, ws_bytes=None, stream=None):
+    d = _dbg(dbg)
+    _check(lib().moe_block_forward(ctypes.byref(shape), ctypes.byref(block), _ptr(x), _ptr(w_router),
+                                   _ptr(router_bias), _ptr(k_per_token), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+                                   _ptr(ws_gate), _ptr(ws_up), _ptr(ws_down), _ptr(out),
+                                   ctypes.byref(d) if d is not None else None, _ptr(ws),
+                                   ws.numel() if ws_bytes is None else ws_bytes, _stream(stream)),
+           "moe_block_forward")
+
+
+def moe_block_forward_int8(shape, block, x, w_router, router_bias, k_per_token, experts, shared, out, dbg, ws,
+                           ws_bytes=None, stream=None):
+    d = _dbg(dbg)
+    _check(lib().moe_block_forward_int8(ctypes.byref(shape), ctypes.byref(block), _ptr(x), _ptr(w_router),
+                                        _ptr(router_bias), _ptr(k_per_token), _mx(experts), _mx(shared), _ptr(out),
+                                        ctypes.byref(d) if d is not None else None, _ptr(ws),
+                                        ws.numel() if ws_bytes is None else ws_bytes, _stream(stream)),
+           "moe_block_forward_int8")

@@ -28,10 +28,14 @@
 //     logical tiles sweep groups of kGroupM row tiles across all column tiles
 //     so the XCD's L2 serves both the token rows and the weight rows.
 // The MXFP8 modes run the same 8-wave schedule on E4M3 codes with the scaled
-// fp8 MFMA (v_mfma_scale_f32_32x32x64_f8f6f4).
+// fp8 MFMA (v_mfma_scale_f32_32x32x64_f8f6f4).  The int8 modes run the bf16
+// schedule on 8-bit codes (v_mfma_i32_32x32x32_i8, int32 sums): a lane's 16
+// bytes of a K slice hold 16 codes where the bf16 modes have 8 elements, so a
+// stage, a fragment and an MFMA's cycles are the same and cover twice the K.
 #include <atomic>
 
 #include "moe_internal.h"
+#include "swiglu.h"
 
 namespace moe {
 namespace {
@@ -42,7 +46,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 // Row tiles per group of the tile order (groups sweep all column tiles; the
 // blocks an XCD runs together then cover about 8 row tiles x 4 column
@@ -162,21 +168,38 @@ __device__ __forceinline__ bool block_tile2(int real0, int real1, int& cls, int&
 //   kGateUpMXPart: the same on MXFP8 operands
 //   kDownW16: kDown with the down weights already fp16 (converted once, ahead
 //            of the layer calls, by the same conversion kDown applies)
+//   kGateUpI8: A = int8 token rows, B0/B1 = int8 gate/up weights, fp32 scales
+//            sa per token row and sb per weight row; out h (fp16) =
+//            silu(sa sb0 A.B0^T) * (sa sb1 A.B1^T), clamped to fp16's range
+//   kDownI8: A = int8 rows, B0 = int8 weights; out (fp32, fp16 or bf16) =
+//            sa sb0 A.B0^T, or with a split K this part's share of it
+//   kGateUpI8Part: the int32 sums A.B0^T at Out and A.B1^T at Out + up_off of
+//            one K range (their sum over the ranges is exact)
+// The int8 modes count K and lda in 16-bit units as the MX modes do.
 enum GemmMode {
   kGateUp = 0, kDown = 1, kPlain = 2, kGateUpMX = 3, kDownMX = 4, kGateUpPart = 5, kGateUpMXPart = 6,
-  kDownW16 = 7
+  kDownW16 = 7, kGateUpI8 = 8, kDownI8 = 9, kGateUpI8Part = 10
 };
 
 // modes that multiply by both the gate and the up weights
 constexpr bool gemm_dual(int MODE) {
-  return MODE == kGateUp || MODE == kGateUpMX || MODE == kGateUpPart || MODE == kGateUpMXPart;
+  return MODE == kGateUp || MODE == kGateUpMX || MODE == kGateUpPart || MODE == kGateUpMXPart ||
+         MODE == kGateUpI8 || MODE == kGateUpI8Part;
 }
 // modes on MXFP8 operands
 constexpr bool gemm_mx(int MODE) { return MODE == kGateUpMX || MODE == kDownMX || MODE == kGateUpMXPart; }
-// split-K gate/up modes (fp32 partial gate and up sums out)
-constexpr bool gemm_part(int MODE) { return MODE == kGateUpPart || MODE == kGateUpMXPart; }
+// modes on int8 operands
+constexpr bool gemm_i8(int MODE) { return MODE == kGateUpI8 || MODE == kDownI8 || MODE == kGateUpI8Part; }
+// split-K gate/up modes (partial gate and up sums out)
+constexpr bool gemm_part(int MODE) {
+  return MODE == kGateUpPart || MODE == kGateUpMXPart || MODE == kGateUpI8Part;
+}
 
-// Scales of the MXFP8 operands (E8M0 bytes, four blocks of a 128-column group
+// Scales of the quantised operands.
+// int8 modes: sa / sb0 / sb1 are fp32 values, sa indexed by token row (through
+// a_rows when the rows are gathered), sb by weight row (expert e's start at
+// e * N), and sout_stride is the moe_dtype of the output (kDownI8).
+// MXFP8 modes: (E8M0 bytes, four blocks of a 128-column group
 // per 32-bit word, words group-major: the word of group g of row r is
 // g * stride + r): token rows (sa), weight rows (sb0 / sb1; expert e's rows
 // start at e * N), and the scales of the h output (sout).
@@ -234,9 +257,17 @@ __device__ __forceinline__ uint32_t f32_to_f16_bits(float f) {
   return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f);
 }
 
+// accumulators of one 32 x 32 fragment
+template <bool I8> struct AccOf { typedef f32x16 type; };
+template <> struct AccOf<true> { typedef i32x16 type; };
+
 template <int MODE>
-__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
-  if constexpr (MODE == kDown || MODE == kDownW16)
+__device__ __forceinline__ typename AccOf<gemm_i8(MODE)>::type mfma32(u32x4 a, u32x4 b,
+                                                                      typename AccOf<gemm_i8(MODE)>::type c) {
+  if constexpr (gemm_i8(MODE))
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0,
+                                                  0, 0);
+  else if constexpr (MODE == kDown || MODE == kDownW16)
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                    __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   else
@@ -302,6 +333,8 @@ __device__ __forceinline__ void gemm_tile(
     int mi, int ni, int kst0, int kstn, long long up_off = 0, bool out_half = false) {
   constexpr bool DUAL = gemm_dual(MODE);
   constexpr bool MX = gemm_mx(MODE);
+  constexpr bool I8 = gemm_i8(MODE);
+  typedef typename AccOf<I8>::type acc_t;
   constexpr int WAVES_M = BM >= 64 ? 2 : 1, WAVES_N = NW / WAVES_M;
   constexpr int WM = BM / WAVES_M, WN = BNB / WAVES_N;
   constexpr int FM = WM / 32, FN = WN / 32;
@@ -317,6 +350,7 @@ __device__ __forceinline__ void gemm_tile(
   static_assert(BM % 32 == 0 && BNB % 32 == 0 && FM >= 1 && FN >= 1, "tile shape");
   static_assert(!PING || NS == 2, "ping-pong uses two LDS stages");
   static_assert(!MX || PING, "MXFP8 modes run the 8-wave schedule");
+  static_assert(!I8 || PING, "int8 modes run the 8-wave schedule");
 
   int expert = 0, row0, rows;
   if (sched) {
@@ -343,16 +377,16 @@ __device__ __forceinline__ void gemm_tile(
   const uint16_t* B0b = B0 + (size_t)expert * strideB + kst0 * kPingRowElems;
   const uint16_t* B1b = DUAL ? B1 + (size_t)expert * strideB + kst0 * kPingRowElems : B0b;
 
-  f32x16 acc0[FN][FM];
-  f32x16 acc1[DUAL ? FN : 1][DUAL ? FM : 1];
+  acc_t acc0[FN][FM];
+  acc_t acc1[DUAL ? FN : 1][DUAL ? FM : 1];
 #pragma unroll
   for (int a = 0; a < FN; ++a)
 #pragma unroll
     for (int b = 0; b < FM; ++b) {
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
-        acc0[a][b][q] = 0.f;
-        if constexpr (DUAL) acc1[a][b][q] = 0.f;
+        acc0[a][b][q] = 0;
+        if constexpr (DUAL) acc1[a][b][q] = 0;
       }
     }
 
@@ -803,6 +837,131 @@ __device__ __forceinline__ void gemm_tile(
         if (fk == 0)
           mx.sout[((size_t)(nb >> 7) * mx.sout_stride + row0 + m) * 4 + ((nb >> 5) & 3)] =
               (uint8_t)sb;
+      }
+    }
+  } else if constexpr (MODE == kGateUpI8) {
+    // fp16 h from the int32 sums, stored as below; N is a multiple of 16, so
+    // a group of four columns is all in or out, a 32-column block may be cut
+    const float* sa = reinterpret_cast<const float*>(mx.sa);
+    const float* sg = reinterpret_cast<const float*>(mx.sb0) + (size_t)expert * N;
+    const float* su = reinterpret_cast<const float*>(mx.sb1) + (size_t)expert * N;
+#pragma unroll
+    for (int b = 0; b < FM; ++b) {
+      const int m = wm * WM + b * 32 + fr;
+      const int rr = row0 + min(m, rows - 1);
+      const float s = sa[a_rows ? a_rows[rr] : rr];
+#pragma unroll
+      for (int a = 0; a < FN; ++a) {
+        const int nb = n0 + wn * WN + a * 32;
+        uint32_t px[4], py[4];
+        bool ovf = false;
+#pragma unroll
+        for (int qi = 0; qi < 4; ++qi) {
+          const int nc = min(nb + 8 * qi + 4 * fk, N - 4);
+          const f32x4 g4 = *reinterpret_cast<const f32x4*>(sg + nc);
+          const f32x4 u4 = *reinterpret_cast<const f32x4*>(su + nc);
+          float h[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            h[q] = silu_mul_exact((float)acc0[a][b][4 * qi + q] * (s * g4[q]),
+                                  (float)acc1[a][b][4 * qi + q] * (s * u4[q]));
+            ovf |= !(fabsf(h[q]) <= 65504.f) && nb + 8 * qi + 4 * fk < N;
+            h[q] = fminf(fmaxf(h[q], -65504.f), 65504.f);
+          }
+          px[qi] = f32_to_f16_bits(h[0]) | (f32_to_f16_bits(h[1]) << 16);
+          py[qi] = f32_to_f16_bits(h[2]) | (f32_to_f16_bits(h[3]) << 16);
+        }
+        const auto x02 = __builtin_amdgcn_permlane32_swap(px[0], px[2], false, false);
+        const auto y02 = __builtin_amdgcn_permlane32_swap(py[0], py[2], false, false);
+        const auto x13 = __builtin_amdgcn_permlane32_swap(px[1], px[3], false, false);
+        const auto y13 = __builtin_amdgcn_permlane32_swap(py[1], py[3], false, false);
+        if (m >= rows) continue;
+        overflow |= ovf;
+        const int nc = nb + 16 * fk;  // this lane's 16 columns
+        if (nc >= N) continue;
+        uint16_t* dst = static_cast<uint16_t*>(Out) + (size_t)(row0 + m) * ldo + nc;
+        *reinterpret_cast<u32x4*>(dst) = u32x4{x02[0], y02[0], x02[1], y02[1]};
+        *reinterpret_cast<u32x4*>(dst + 8) = u32x4{x13[0], y13[0], x13[1], y13[1]};
+      }
+    }
+  } else if constexpr (MODE == kDownI8) {
+    // y = sa sb (int32 sum), fp32 as four-column runs, or 16-bit values
+    // exchanged between lane halves and stored 16 columns per lane
+    const float* sa = reinterpret_cast<const float*>(mx.sa);
+    const float* sb = reinterpret_cast<const float*>(mx.sb0) + (size_t)expert * N;
+    const int ydt = mx.sout_stride;
+#pragma unroll
+    for (int b = 0; b < FM; ++b) {
+      const int m = wm * WM + b * 32 + fr;
+      const float s = sa[row0 + min(m, rows - 1)];
+#pragma unroll
+      for (int a = 0; a < FN; ++a) {
+        const int nb = n0 + wn * WN + a * 32;
+        f32x4 v[4];
+#pragma unroll
+        for (int qi = 0; qi < 4; ++qi) {
+          const f32x4 b4 = *reinterpret_cast<const f32x4*>(sb + min(nb + 8 * qi + 4 * fk, N - 4));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[qi][q] = (float)acc0[a][b][4 * qi + q] * (s * b4[q]);
+        }
+        if (ydt == MOE_F32) {
+          if (m >= rows) continue;
+#pragma unroll
+          for (int qi = 0; qi < 4; ++qi) {
+            const int n = nb + 8 * qi + 4 * fk;
+            if (n < N) *reinterpret_cast<f32x4*>(static_cast<float*>(Out) + (size_t)(row0 + m) * ldo + n) = v[qi];
+          }
+          continue;
+        }
+        uint32_t px[4], py[4];
+        bool ovf = false;
+#pragma unroll
+        for (int qi = 0; qi < 4; ++qi) {
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (ydt == MOE_F16) {
+              ovf |= !(fabsf(v[qi][q]) <= 65504.f) && nb + 8 * qi + 4 * fk < N;
+              w[q] = f32_to_f16_bits(v[qi][q]);
+            } else {
+              w[q] = f32_to_bf16_rne(v[qi][q]);
+            }
+          }
+          px[qi] = w[0] | (w[1] << 16);
+          py[qi] = w[2] | (w[3] << 16);
+        }
+        const auto x02 = __builtin_amdgcn_permlane32_swap(px[0], px[2], false, false);
+        const auto y02 = __builtin_amdgcn_permlane32_swap(py[0], py[2], false, false);
+        const auto x13 = __builtin_amdgcn_permlane32_swap(px[1], px[3], false, false);
+        const auto y13 = __builtin_amdgcn_permlane32_swap(py[1], py[3], false, false);
+        if (m >= rows) continue;
+        overflow |= ovf;
+        const int nc = nb + 16 * fk;
+        if (nc >= N) continue;
+        uint16_t* dst = static_cast<uint16_t*>(Out) + (size_t)(row0 + m) * ldo + nc;
+        *reinterpret_cast<u32x4*>(dst) = u32x4{x02[0], y02[0], x02[1], y02[1]};
+        *reinterpret_cast<u32x4*>(dst + 8) = u32x4{x13[0], y13[0], x13[1], y13[1]};
+      }
+    }
+  } else if constexpr (MODE == kGateUpI8Part) {
+#pragma unroll
+    for (int b = 0; b < FM; ++b) {
+      const int m = wm * WM + b * 32 + fr;
+      if (m >= rows) continue;
+#pragma unroll
+      for (int a = 0; a < FN; ++a) {
+#pragma unroll
+        for (int qi = 0; qi < 4; ++qi) {
+          const int n = n0 + wn * WN + a * 32 + 8 * qi + 4 * fk;
+          if (n >= N) continue;
+          int* dst = static_cast<int*>(Out) + (size_t)(row0 + m) * ldo + n;
+#pragma unroll
+          for (int ob = 0; ob < 2; ++ob) {
+            const acc_t acc = ob ? acc1[a][b] : acc0[a][b];
+            *reinterpret_cast<i32x4*>(dst + (ob ? up_off : 0)) =
+                i32x4{acc[4 * qi], acc[4 * qi + 1], acc[4 * qi + 2], acc[4 * qi + 3]};
+          }
+        }
       }
     }
   } else if constexpr (MODE == kGateUp) {
@@ -1703,6 +1862,80 @@ hipError_t launch_gemm_down_mx2(const void* A, const uint8_t* hsc, int hs_stride
   const MxArgs mx{hsc, sb_w, nullptr, nullptr, hs_stride, sb_stride, 0};
   return launch_mfma2<256, 256, kMergedSmallRows, 256, kDownMX>(A, nullptr, K / 2, B, nullptr, N, K / 2, Y, ldy, flags, sb,
                                                   cb, mb, ss, cs, ms, st, mx, ksplit, part_elems, y_half);
+}
+
+// ---- int8 operands: codes (K counted in 16-bit units inside), fp32 scales ----
+hipError_t launch_gemm_gateup_i8(int bm, const void* A, const int32_t* a_rows, const float* sa, const void* Bg,
+                                 const float* sbg, const void* Bu, const float* sbu, int N, int K, void* h,
+                                 const MTile* sched, const int32_t* count, int max_tiles, int static_rows,
+                                 uint32_t* flags, hipStream_t st) {
+  const int mslots = sched ? max_tiles : (static_rows + bm - 1) / bm;
+  if (mslots == 0) return hipSuccess;
+  const MxArgs mx{reinterpret_cast<const uint8_t*>(sa), reinterpret_cast<const uint8_t*>(sbg),
+                  reinterpret_cast<const uint8_t*>(sbu), nullptr, 0, 0, 0, 0};
+  const int K2 = K / 2;
+  if (bm == 256)
+    return launch_mfma<256, 128, kGateUpI8, 2, 8>(A, a_rows, K2, Bg, Bu, N, K2, h, N, nullptr, sched, count, mslots,
+                                                  static_rows, flags, st, mx);
+  if (bm == 128)
+    return launch_mfma<128, 128, kGateUpI8, 2, 8>(A, a_rows, K2, Bg, Bu, N, K2, h, N, nullptr, sched, count, mslots,
+                                                  static_rows, flags, st, mx);
+  if (bm != 32) return hipErrorInvalidValue;
+  return launch_mfma<32, 256, kGateUpI8, 2, 8>(A, a_rows, K2, Bg, Bu, N, K2, h, N, nullptr, sched, count, mslots,
+                                               static_rows, flags, st, mx);
+}
+
+hipError_t launch_gemm_gateup_i8_parts(const void* A, const int32_t* a_rows, const void* Bg, const void* Bu, int N,
+                                       int K, int32_t* parts, const MTile* sched, const int32_t* count,
+                                       int max_tiles, int static_rows, int ksplit, long long part_elems,
+                                       hipStream_t st) {
+  const int mslots = sched ? max_tiles : (static_rows + 31) / 32;
+  if (mslots == 0) return hipSuccess;
+  return launch_mfma<32, 256, kGateUpI8Part, 2, 8>(A, a_rows, K / 2, Bg, Bu, N, K / 2, parts, N, nullptr, sched,
+                                                   count, mslots, static_rows, nullptr, st, MxArgs{}, ksplit,
+                                                   part_elems);
+}
+
+hipError_t launch_gemm_down_i8(int bm, const void* A, const float* sa, const void* B, const float* sb, int N, int K,
+                               int y_dtype, void* Y, const MTile* sched, const int32_t* count, int max_tiles,
+                               int static_rows, uint32_t* flags, hipStream_t st, int ksplit,
+                               long long part_elems) {
+  const int mslots = sched ? max_tiles : (static_rows + bm - 1) / bm;
+  if (mslots == 0) return hipSuccess;
+  if (ksplit > 1 && y_dtype != MOE_F32) return hipErrorInvalidValue;
+  const MxArgs mx{reinterpret_cast<const uint8_t*>(sa), reinterpret_cast<const uint8_t*>(sb), nullptr, nullptr, 0,
+                  0, y_dtype, 0};
+  const int K2 = K / 2;
+  if (bm == 256)
+    return launch_mfma<256, 256, kDownI8, 2, 8>(A, nullptr, K2, B, nullptr, N, K2, Y, N, nullptr, sched, count,
+                                                mslots, static_rows, flags, st, mx, ksplit, part_elems);
+  if (bm == 128)
+    return launch_mfma<128, 128, kDownI8, 2, 8>(A, nullptr, K2, B, nullptr, N, K2, Y, N, nullptr, sched, count,
+                                                mslots, static_rows, flags, st, mx, ksplit, part_elems);
+  if (bm != 32) return hipErrorInvalidValue;
+  return launch_mfma<32, 256, kDownI8, 2, 8>(A, nullptr, K2, B, nullptr, N, K2, Y, N, nullptr, sched, count, mslots,
+                                             static_rows, flags, st, mx, ksplit, part_elems);
+}
+
+hipError_t launch_gemm_gateup_i8_2(const void* A, const int32_t* a_rows, const float* sa, const void* Bg,
+                                   const float* sbg, const void* Bu, const float* sbu, int N, int K, void* h,
+                                   const MTile* sb, const int32_t* cb, int mb, const MTile* ss, const int32_t* cs,
+                                   int ms, uint32_t* flags, hipStream_t st) {
+  const MxArgs mx{reinterpret_cast<const uint8_t*>(sa), reinterpret_cast<const uint8_t*>(sbg),
+                  reinterpret_cast<const uint8_t*>(sbu), nullptr, 0, 0, 0, 0};
+  return launch_mfma2<256, 128, kMergedSmallRows, 256, kGateUpI8>(A, a_rows, K / 2, Bg, Bu, N, K / 2, h, N, flags,
+                                                                  sb, cb, mb, ss, cs, ms, st, mx);
+}
+
+hipError_t launch_gemm_down_i8_2(const void* A, const float* sa, const void* B, const float* sb_w, int N, int K,
+                                 int y_dtype, void* Y, const MTile* sb, const int32_t* cb, int mb, const MTile* ss,
+                                 const int32_t* cs, int ms, uint32_t* flags, hipStream_t st, int ksplit,
+                                 long long part_elems) {
+  if (ksplit > 1 && y_dtype != MOE_F32) return hipErrorInvalidValue;
+  const MxArgs mx{reinterpret_cast<const uint8_t*>(sa), reinterpret_cast<const uint8_t*>(sb_w), nullptr, nullptr, 0,
+                  0, y_dtype, 0};
+  return launch_mfma2<256, 256, kMergedSmallRows, 256, kDownI8>(A, nullptr, K / 2, B, nullptr, N, K / 2, Y, N, flags,
+                                                                sb, cb, mb, ss, cs, ms, st, mx, ksplit, part_elems);
 }
 
 }  // namespace moe

@@ -111,6 +111,58 @@ moe_status check_mx_ffn(const moe_mxfp8_ffn* w) {
   return MOE_OK;
 }
 
+// int8 layers: bf16 x and router, K of both products in whole 128-byte rows,
+// int32 sums (127 * 127 * K < 2^31)
+constexpr int kMaxInt8K = 131072;
+
+moe_status check_int8_shape(const moe_shape* s) {
+  MOE_TRY(check_shape(s));
+  if (s->act_dtype != MOE_BF16 || s->down_dtype == MOE_F16) return MOE_ERR_UNSUPPORTED;
+  if (s->hidden % 128 || s->intermediate % 128 || s->shared_intermediate % 128) return MOE_ERR_UNSUPPORTED;
+  if (s->hidden > kMaxInt8K || s->intermediate > kMaxInt8K || s->shared_intermediate > kMaxInt8K)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_int8_ffn(const moe_int8_ffn* w) {
+  if (!w) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(w->gate));
+  MOE_TRY(need(w->gate_scales));
+  MOE_TRY(need(w->up));
+  MOE_TRY(need(w->up_scales));
+  MOE_TRY(need(w->down));
+  MOE_TRY(need(w->down_scales));
+  return MOE_OK;
+}
+
+inline bool is_float_type(int dt) { return dt == MOE_F32 || dt == MOE_F16 || dt == MOE_BF16; }
+inline bool is_stream_type(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
+inline moe_status opt16(const void* p) { return p ? need(p) : MOE_OK; }
+
+// The parts of a block's description that the end of the block reads.
+moe_status check_block_end(const moe_block* b) {
+  if (!b) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(opt16(b->post_norm));
+  if (!(b->eps > 0.0f) || !std::isfinite(b->eps) || !std::isfinite(b->residual_scale)) return MOE_ERR_INVALID_ARG;
+  if (!is_stream_type(b->stream_dtype)) return MOE_ERR_INVALID_ARG;
+  if (b->gate) {
+    if (!is_stream_type(b->gate_dtype)) return MOE_ERR_INVALID_ARG;
+    if (b->gate_row_stride < 0 || (b->gate_col_stride != 0 && b->gate_col_stride != 1)) return MOE_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(b->gate) & (b->gate_dtype == MOE_F32 ? 3u : 1u)) return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+// Both ends, and the stream the layer can start from.
+moe_status check_block(const moe_shape& s, const moe_block* b) {
+  MOE_TRY(check_block_end(b));
+  MOE_TRY(opt4(b->select_bias));
+  MOE_TRY(opt16(b->pre_norm));
+  if (!b->pre_norm && b->stream_dtype != s.act_dtype) return MOE_ERR_UNSUPPORTED;
+  if (b->stream_dtype == MOE_BF16 && s.hidden % 8) return MOE_ERR_UNSUPPORTED;  // (fp32 layers)
+  return MOE_OK;
+}
+
 // Records the stage event when the caller asked for it.
 inline hipError_t stage_mark(const moe_debug* d, int stage, bool start, hipStream_t st) {
   if (!d) return hipSuccess;
@@ -274,7 +326,8 @@ int gate_up_parts(long long blocks, int stages, bool rounds) {
 
 }  // namespace
 
-WsLayout plan_workspace(const moe_shape& s, bool mx) {
+WsLayout plan_workspace(const moe_shape& s, int format, bool normed) {
+  const bool mx = format == kExpertsMX, i8 = format == kExpertsI8;
   WsLayout w{};
   const size_t T = (size_t)s.num_tokens, E = (size_t)s.num_experts, k = (size_t)s.top_k;
   const size_t H = (size_t)s.hidden, I = (size_t)s.intermediate, Is = (size_t)s.shared_intermediate;
@@ -283,10 +336,10 @@ WsLayout plan_workspace(const moe_shape& s, bool mx) {
   const GemmPlan gp = choose_gemm_plan(s);
   w.n_dispatch_tiles = (int)((slots + kDispatchTileSlots - 1) / kDispatchTileSlots);
   tile_bounds(s, gp, w.max_tiles_big, w.max_tiles_small);
-  w.ksplit = down_parts(s, gp, w.max_tiles_small, mx);
+  w.ksplit = down_parts(s, gp, w.max_tiles_small, mx || i8);
   w.ks_gu = w.ks_gus = 1;
   if (s.act_dtype == MOE_BF16) {
-    const int stages = (int)(H / (mx ? 128 : 64));  // K stages (128 codes, or 64 bf16 elements)
+    const int stages = (int)(H / (mx || i8 ? 128 : 64));  // K stages (128 codes, or 64 bf16 elements)
     // routed experts of a token or a few (decode plans only)
     if (!gp.has_big() && gp.has_small())
       w.ks_gu = gate_up_parts(std::min<long long>(w.max_tiles_small, few_row_tiles(s)) *
@@ -330,6 +383,14 @@ WsLayout plan_workspace(const moe_shape& s, bool mx) {
     w.hsc = take(slots * I / 32);
     w.hssc = take(T * Is / 32);
   }
+  if (i8) {
+    w.xq = take(T * H);
+    w.xsc = take(T * 4);
+    w.hq = take(std::max(slots * I, T * Is));
+    w.hsc = take(slots * 4);
+    w.hssc = take(T * 4);
+  }
+  if (normed) w.xn = take(T * H * (size_t)elem_bytes(s.act_dtype));
   w.total = o;
   return w;
 }
@@ -536,6 +597,122 @@ moe_status run_shared(const moe_shape& s, const void* x, const void* wsg, const 
   return MOE_OK;
 }
 
+// int8 S7-S8: xq rows (gathered through a_rows when given, their scales too).
+// With y_dtype fp32 and ksplit > 1, y holds ksplit partial sums.
+moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows, const float* xsc,
+                      const int32_t* offsets, const moe_int8_ffn& w, int y_dtype, void* y, void* ws,
+                      const WsLayout& L, hipStream_t st, const moe_debug* dbg, int ksplit) {
+  const GemmPlan gp = choose_gemm_plan(s);
+  const int E = s.num_experts, H = s.hidden, I = s.intermediate;
+  const int slots = s.num_tokens * s.top_k;
+  MTile* sb = at<MTile>(ws, L.sched_big);
+  MTile* ss = at<MTile>(ws, L.sched_small);
+  int32_t* cnt = at<int32_t>(ws, L.sched_count);
+  uint32_t* flags = at<uint32_t>(ws, L.flags);
+  void* h = at<void>(ws, L.h);
+  void* hq = at<void>(ws, L.hq);
+  float* hsc = at<float>(ws, L.hsc);
+  const bool merged = gp.has_big() && gp.has_small();
+  MOE_HIP(launch_build_schedule(offsets, E, gp, sb, L.max_tiles_big, ss, L.max_tiles_small, cnt, st));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, true, st));
+  if (merged) {
+    MOE_HIP(launch_gemm_gateup_i8_2(xq, a_rows, xsc, w.gate, w.gate_scales, w.up, w.up_scales, I, H, h, sb, cnt,
+                                    L.max_tiles_big, ss, cnt + 1, L.max_tiles_small, flags, st));
+  } else if (L.ks_gu > 1) {
+    int32_t* parts = at<int32_t>(ws, L.gu_parts);
+    const long long pe = (long long)slots * I;
+    MOE_HIP(launch_gemm_gateup_i8_parts(xq, a_rows, w.gate, w.up, I, H, parts, ss, cnt + 1, L.max_tiles_small, 0,
+                                        L.ks_gu, pe, st));
+    MOE_HIP(launch_swiglu_parts_i8(parts, L.ks_gu, pe, I, a_rows, xsc, w.gate_scales, w.up_scales, ss, cnt + 1,
+                                   L.max_tiles_small, 0, h, flags, st));
+  } else {
+    MOE_HIP(launch_gemm_gateup_i8(gp.bm_small, xq, a_rows, xsc, w.gate, w.gate_scales, w.up, w.up_scales, I, H, h,
+                                  ss, cnt + 1, L.max_tiles_small, 0, flags, st));
+  }
+  MOE_HIP(launch_quant_int8(MOE_F16, h, slots, I, offsets + E, hq, hsc, st));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, false, st));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_DOWN, true, st));
+  const long long pe = (long long)slots * H;
+  if (merged)
+    MOE_HIP(launch_gemm_down_i8_2(hq, hsc, w.down, w.down_scales, H, I, y_dtype, y, sb, cnt, L.max_tiles_big, ss,
+                                  cnt + 1, L.max_tiles_small, flags, st, ksplit, pe));
+  else
+    MOE_HIP(launch_gemm_down_i8(gp.bm_small, hq, hsc, w.down, w.down_scales, H, I, y_dtype, y, ss, cnt + 1,
+                                L.max_tiles_small, 0, flags, st, ksplit, pe));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_DOWN, false, st));
+  return MOE_OK;
+}
+
+// int8 shared expert on all T quantised rows
+moe_status run_shared_i8(const moe_shape& s, const void* xq, const float* xsc, const moe_int8_ffn& w, int y_dtype,
+                         void* ws, const WsLayout& L, hipStream_t st) {
+  const int T = s.num_tokens, H = s.hidden, Is = s.shared_intermediate;
+  const int bm = T >= 2048 ? 256 : (T >= 128 ? 128 : 32);
+  void* hs = at<void>(ws, L.hs);
+  float* hssc = at<float>(ws, L.hssc);
+  uint32_t* flags = at<uint32_t>(ws, L.flags);
+  if (L.ks_gus > 1 && bm == 32) {
+    int32_t* parts = at<int32_t>(ws, L.gu_parts);
+    const long long pe = (long long)T * Is;
+    MOE_HIP(launch_gemm_gateup_i8_parts(xq, nullptr, w.gate, w.up, Is, H, parts, nullptr, nullptr, 0, T, L.ks_gus,
+                                        pe, st));
+    MOE_HIP(launch_swiglu_parts_i8(parts, L.ks_gus, pe, Is, nullptr, xsc, w.gate_scales, w.up_scales, nullptr,
+                                   nullptr, 0, T, hs, flags, st));
+  } else {
+    MOE_HIP(launch_gemm_gateup_i8(bm, xq, nullptr, xsc, w.gate, w.gate_scales, w.up, w.up_scales, Is, H, hs, nullptr,
+                                  nullptr, 0, T, flags, st));
+  }
+  MOE_HIP(launch_quant_int8(MOE_F16, hs, T, Is, nullptr, at<void>(ws, L.hq), hssc, st));
+  MOE_HIP(launch_gemm_down_i8(bm, at<void>(ws, L.hq), hssc, w.down, w.down_scales, H, Is, y_dtype,
+                              at<void>(ws, L.ys), nullptr, nullptr, 0, T, flags, st));
+  return MOE_OK;
+}
+
+// ---- one grouped int8 product ---------------------------------------------------
+// Planned as the down projection of a layer with one slot per row.
+struct GemmI8Plan {
+  moe_shape s;
+  GemmPlan gp;
+  int max_big, max_small, ksplit;
+  size_t flags, sched_big, sched_small, sched_count, parts, total;
+};
+
+GemmI8Plan plan_gemm_i8(int rows, int n, int k, int E) {
+  GemmI8Plan p{};
+  p.s.num_tokens = rows;
+  p.s.hidden = n;
+  p.s.intermediate = k;
+  p.s.num_experts = E;
+  p.s.top_k = 1;
+  p.s.num_groups = 1;
+  p.s.act_dtype = MOE_BF16;
+  p.gp = choose_gemm_plan(p.s);
+  tile_bounds(p.s, p.gp, p.max_big, p.max_small);
+  p.ksplit = down_parts(p.s, p.gp, p.max_small, true);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at_ = o;
+    o = align_up(o + bytes, 256);
+    return at_;
+  };
+  p.flags = take(256);
+  p.sched_big = take((size_t)p.max_big * sizeof(MTile));
+  p.sched_small = take((size_t)p.max_small * sizeof(MTile));
+  p.sched_count = take(16);
+  p.parts = take(p.ksplit > 1 ? (size_t)p.ksplit * rows * n * 4 : 0);
+  p.total = o;
+  return p;
+}
+
+moe_status check_gemm_i8(int32_t rows, int32_t n, int32_t k, int32_t E) {
+  if (rows < 0 || n <= 0 || k <= 0 || E < 1) return MOE_ERR_INVALID_ARG;
+  if (E > kMaxExperts || n % 16 || k % 128 || k > kMaxInt8K) return MOE_ERR_UNSUPPORTED;
+  // offsets inside one expert's weights and inside the rows' int32 indices
+  if ((long long)n * k > (long long)INT_MAX || (long long)E * n > (long long)INT_MAX || rows > INT_MAX / 2)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 // ---- the layer, shared by the workspace and the no-allocation entry points ---
 
 // Host checks of moe_layer_forward's arguments (all but the workspace).
@@ -619,6 +796,105 @@ moe_status run_layer(const moe_shape& s, const void* x, const void* w_router, co
   MOE_HIP(stage_mark(dbg, MOE_STAGE_COMBINE, true, st));
   MOE_HIP(launch_combine(s, y, ros, gates, ys, out, st, L.ksplit,
                          (long long)s.num_tokens * s.top_k * s.hidden, y_half));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_COMBINE, false, st));
+  return MOE_OK;
+}
+
+// ---- the block around the layer --------------------------------------------------
+
+// Host checks of the arguments both block calls share (all but the workspace
+// and the experts' weights).
+moe_status check_block_args(const moe_shape& s, const moe_block* block, const void* x, const void* w_router,
+                            const float* router_bias, const int32_t* k_per_token, const void* out,
+                            const moe_debug* dbg) {
+  MOE_TRY(check_block(s, block));
+  MOE_TRY(need(x));
+  MOE_TRY(need(w_router));
+  MOE_TRY(opt4(router_bias));
+  MOE_TRY(opt4(k_per_token));
+  MOE_TRY(need(out));
+  if (dbg) {
+    if (dbg->logits) MOE_TRY(need(dbg->logits));
+    MOE_TRY(opt4(dbg->topk_ids));
+    MOE_TRY(opt4(dbg->topk_gates));
+    MOE_TRY(opt4(dbg->expert_counts));
+    MOE_TRY(opt4(dbg->expert_offsets));
+    MOE_TRY(opt4(dbg->row_of_slot));
+    MOE_TRY(opt4(dbg->num_dropped));
+    MOE_TRY(opt4(dbg->row_token));
+  }
+  return MOE_OK;
+}
+
+// The block on validated arguments, T > 0.  Experts: the bf16 / fp32 weights of
+// `wt` (gate, up, down, shared gate, up, down), or the int8 ones when experts
+// is given.
+moe_status run_block(const moe_shape& s, const moe_block& b, const void* x, const void* w_router,
+                     const float* router_bias, const int32_t* k_per_token, const void* const* wt,
+                     const moe_int8_ffn* experts, const moe_int8_ffn* shared, void* out, const moe_debug* dbg,
+                     void* ws, const WsLayout& L, hipStream_t st) {
+  const int T = s.num_tokens, H = s.hidden;
+  float* logits = (dbg && dbg->logits) ? dbg->logits : at<float>(ws, L.logits);
+  int32_t* ids = (dbg && dbg->topk_ids) ? dbg->topk_ids : at<int32_t>(ws, L.ids);
+  float* gates = (dbg && dbg->topk_gates) ? dbg->topk_gates : at<float>(ws, L.gates);
+  int32_t* counts = (dbg && dbg->expert_counts) ? dbg->expert_counts : at<int32_t>(ws, L.counts);
+  int32_t* offsets = (dbg && dbg->expert_offsets) ? dbg->expert_offsets : at<int32_t>(ws, L.offsets);
+  int32_t* ros = (dbg && dbg->row_of_slot) ? dbg->row_of_slot : at<int32_t>(ws, L.row_of_slot);
+  int32_t* nd = (dbg && dbg->num_dropped) ? dbg->num_dropped : at<int32_t>(ws, L.num_dropped);
+  int32_t* row_token = (dbg && dbg->row_token) ? dbg->row_token : at<int32_t>(ws, L.row_token);
+  uint32_t* flags = at<uint32_t>(ws, L.flags);
+  void* y = at<void>(ws, L.y);
+  // expert outputs reach the end of the block as fp16 unless a split
+  // projection leaves partial sums (or the layer is fp32)
+  const bool y_half = s.act_dtype == MOE_BF16 && L.ksplit == 1;
+  const int y_dtype = y_half ? MOE_F16 : MOE_F32;
+  void* xq = experts ? at<void>(ws, L.xq) : nullptr;
+  float* xsc = experts ? at<float>(ws, L.xsc) : nullptr;
+
+  const void* xl = x;  // what the layer takes
+  if (b.pre_norm) {
+    void* xn = at<void>(ws, L.xn);
+    MOE_HIP(launch_norm(T, H, b.stream_dtype, x, b.pre_norm, b.eps, s.act_dtype, xn, xq, xsc, st));
+    xl = xn;
+  }
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_ROUTER, true, st));
+  int rparts = 1;
+  float* lparts = at<float>(ws, L.logits_parts);
+  MOE_TRY(run_router(s, xl, w_router, router_bias, logits, flags, st, lparts, rparts));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_ROUTER, false, st));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_ROUTE, true, st));
+  const float* lg = rparts > 1 ? lparts : logits;
+  float* sum_out = rparts > 1 ? logits : nullptr;
+  const long long pstride = (long long)T * s.num_experts;
+  if (b.select_bias)
+    MOE_HIP(launch_route_biased(s, lg, b.select_bias, k_per_token, ids, gates, flags, st, rparts, pstride, sum_out));
+  else
+    MOE_HIP(launch_route_topk(s, lg, k_per_token, ids, gates, flags, st, rparts, pstride, sum_out));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_ROUTE, false, st));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_DISPATCH, true, st));
+  MOE_HIP(launch_dispatch(s, ids, counts, offsets, ros, row_token, nd, at<int32_t>(ws, L.tile_counts),
+                          L.n_dispatch_tiles, flags, st));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_DISPATCH, false, st));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_GATHER, true, st));
+  if (experts && !b.pre_norm) MOE_HIP(launch_quant_int8(MOE_BF16, x, T, H, nullptr, xq, xsc, st));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_GATHER, false, st));
+  if (experts)
+    MOE_TRY(run_ffn_i8(s, xq, row_token, xsc, offsets, *experts, y_dtype, y, ws, L, st, dbg, L.ksplit));
+  else
+    MOE_TRY(run_ffn(s, xl, row_token, offsets, wt[0], wt[1], wt[2], y, ws, L, st, dbg, L.ksplit, y_half));
+  const void* ys = nullptr;
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_SHARED, true, st));
+  if (s.shared_intermediate > 0) {
+    if (experts)
+      MOE_TRY(run_shared_i8(s, xq, xsc, *shared, y_dtype, ws, L, st));
+    else
+      MOE_TRY(run_shared(s, xl, wt[3], wt[4], wt[5], ws, L, st, y_half));
+    ys = at<void>(ws, L.ys);
+  }
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_SHARED, false, st));
+  MOE_HIP(stage_mark(dbg, MOE_STAGE_COMBINE, true, st));
+  MOE_HIP(launch_combine_norm(s, b, y_dtype, y, ros, gates, ys, x, out, st, L.ksplit,
+                              (long long)T * s.top_k * H));
   MOE_HIP(stage_mark(dbg, MOE_STAGE_COMBINE, false, st));
   return MOE_OK;
 }
@@ -921,7 +1197,7 @@ moe_status moe_convert_bf16_to_f16(int64_t n, const void* src, void* dst, void* 
 moe_status moe_workspace_size_mxfp8(const moe_shape* shape, size_t* bytes) {
   MOE_TRY(check_mx_shape(shape));
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  *bytes = plan_workspace(*shape, true).total;
+  *bytes = plan_workspace(*shape, kExpertsMX).total;
   return MOE_OK;
 }
 
@@ -938,7 +1214,7 @@ moe_status moe_grouped_ffn_mxfp8(const moe_shape* shape, const void* x_codes,
   MOE_TRY(need(y_perm));
   MOE_TRY(need(ws));
   if ((long long)x_scale_stride < (long long)s.num_tokens * s.top_k) return MOE_ERR_INVALID_ARG;
-  const WsLayout L = plan_workspace(s, true);
+  const WsLayout L = plan_workspace(s, kExpertsMX);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   if (s.num_tokens == 0) return MOE_OK;
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -972,7 +1248,7 @@ moe_status moe_layer_forward_mxfp8(const moe_shape* shape, const void* x, const 
     MOE_TRY(opt4(dbg->num_dropped));
     MOE_TRY(opt4(dbg->row_token));
   }
-  const WsLayout L = plan_workspace(s, true);
+  const WsLayout L = plan_workspace(s, kExpertsMX);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   if (s.num_tokens == 0) return MOE_OK;
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -1026,6 +1302,233 @@ moe_status moe_layer_forward_mxfp8(const moe_shape* shape, const void* x, const 
                          (long long)s.num_tokens * s.top_k * s.hidden));
   MOE_HIP(stage_mark(dbg, MOE_STAGE_COMBINE, false, st));
   return MOE_OK;
+}
+
+moe_status moe_route_biased(const moe_shape* shape, const void* x, const void* w_router,
+                            const float* router_bias, const float* select_bias, const float* logits_in,
+                            float* logits_out, const int32_t* k_per_token, int32_t* topk_ids,
+                            float* topk_gates, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_shape(shape));
+  const moe_shape& s = *shape;
+  if (logits_in) {
+    MOE_TRY(need4(logits_in));
+  } else {
+    MOE_TRY(need(x));
+    MOE_TRY(need(w_router));
+    MOE_TRY(opt4(router_bias));
+  }
+  if (logits_out) MOE_TRY(need(logits_out));
+  MOE_TRY(need4(select_bias));
+  MOE_TRY(opt4(k_per_token));
+  MOE_TRY(need4(topk_ids));
+  MOE_TRY(need4(topk_gates));
+  MOE_TRY(need(ws));
+  const WsLayout L = plan_workspace(s);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (s.num_tokens == 0) return MOE_OK;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  uint32_t* flags = at<uint32_t>(ws, L.flags);
+  const float* logits = logits_in;
+  int rparts = 1;
+  float* sum_out = nullptr;
+  if (!logits) {
+    float* lo = logits_out ? logits_out : at<float>(ws, L.logits);
+    float* pb = at<float>(ws, L.logits_parts);
+    MOE_TRY(run_router(s, x, w_router, router_bias, lo, flags, st, pb, rparts));
+    logits = rparts > 1 ? pb : lo;
+    sum_out = rparts > 1 ? lo : nullptr;
+  } else {
+    MOE_HIP(launch_clear_flags(flags, st));
+  }
+  MOE_HIP(launch_route_biased(s, logits, select_bias, k_per_token, topk_ids, topk_gates, flags, st, rparts,
+                              (long long)s.num_tokens * s.num_experts, sum_out));
+  return MOE_OK;
+}
+
+moe_status moe_quantize_int8(int32_t rows, int32_t cols, int32_t src_dtype, const void* src, int8_t* codes,
+                             float* scales, void* stream) {
+  if (rows < 0 || cols <= 0 || !is_float_type(src_dtype)) return MOE_ERR_INVALID_ARG;
+  if (cols % 128) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(need(src));
+  MOE_TRY(need(codes));
+  MOE_TRY(need4(scales));
+  if (rows == 0) return MOE_OK;
+  MOE_HIP(launch_quant_int8(src_dtype, src, rows, cols, nullptr, codes, scales, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_workspace_size_gemm_int8(int32_t rows, int32_t n, int32_t k, int32_t num_experts, size_t* bytes) {
+  MOE_TRY(check_gemm_i8(rows, n, k, num_experts));
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = plan_gemm_i8(rows, n, k, num_experts).total;
+  return MOE_OK;
+}
+
+moe_status moe_grouped_gemm_int8(int32_t rows, int32_t n, int32_t k, int32_t num_experts, const int8_t* a,
+                                 const float* a_scales, const int32_t* expert_offsets, const int8_t* b,
+                                 const float* b_scales, int32_t y_dtype, void* y, void* ws, size_t ws_bytes,
+                                 void* stream) {
+  MOE_TRY(check_gemm_i8(rows, n, k, num_experts));
+  if (!is_float_type(y_dtype)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(a));
+  MOE_TRY(need4(a_scales));
+  if (!expert_offsets && num_experts != 1) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(opt4(expert_offsets));
+  MOE_TRY(need(b));
+  MOE_TRY(need(b_scales));
+  MOE_TRY(need(y));
+  MOE_TRY(need(ws));
+  const GemmI8Plan p = plan_gemm_i8(rows, n, k, num_experts);
+  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
+  if (rows == 0) return MOE_OK;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  uint32_t* flags = at<uint32_t>(ws, p.flags);
+  MTile* sb = at<MTile>(ws, p.sched_big);
+  MTile* ss = at<MTile>(ws, p.sched_small);
+  int32_t* cnt = at<int32_t>(ws, p.sched_count);
+  const long long pe = (long long)rows * n;
+  const bool split = p.ksplit > 1;
+  void* dst = split ? at<void>(ws, p.parts) : y;
+  const int dt = split ? MOE_F32 : y_dtype;
+  MOE_HIP(launch_clear_flags(flags, st));
+  if (!expert_offsets) {
+    const int bm = rows >= 2048 ? 256 : (rows >= 128 ? 128 : 32);
+    MOE_HIP(launch_gemm_down_i8(bm, a, a_scales, b, b_scales, n, k, dt, dst, nullptr, nullptr, 0, rows, flags, st,
+                                p.ksplit, pe));
+  } else {
+    MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sb, p.max_big, ss, p.max_small, cnt, st));
+    if (p.gp.has_big() && p.gp.has_small())
+      MOE_HIP(launch_gemm_down_i8_2(a, a_scales, b, b_scales, n, k, dt, dst, sb, cnt, p.max_big, ss, cnt + 1,
+                                    p.max_small, flags, st, p.ksplit, pe));
+    else
+      MOE_HIP(launch_gemm_down_i8(p.gp.bm_small, a, a_scales, b, b_scales, n, k, dt, dst, ss, cnt + 1, p.max_small,
+                                  0, flags, st, p.ksplit, pe));
+  }
+  if (split)
+    MOE_HIP(launch_sum_parts(at<float>(ws, p.parts), p.ksplit, pe, n,
+                             expert_offsets ? expert_offsets + num_experts : nullptr, rows, y_dtype, y, flags, st));
+  return MOE_OK;
+}
+
+moe_status moe_workspace_size_int8(const moe_shape* shape, size_t* bytes) {
+  MOE_TRY(check_int8_shape(shape));
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = plan_workspace(*shape, kExpertsI8, true).total;
+  return MOE_OK;
+}
+
+moe_status moe_grouped_ffn_int8(const moe_shape* shape, const int8_t* x_codes, const float* x_scales,
+                                const int32_t* expert_offsets, const moe_int8_ffn* experts, int32_t y_dtype,
+                                void* y_perm, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_int8_shape(shape));
+  const moe_shape& s = *shape;
+  if (!is_float_type(y_dtype)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(x_codes));
+  MOE_TRY(need4(x_scales));
+  MOE_TRY(need4(expert_offsets));
+  MOE_TRY(check_int8_ffn(experts));
+  MOE_TRY(need(y_perm));
+  MOE_TRY(need(ws));
+  const WsLayout L = plan_workspace(s, kExpertsI8, true);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (s.num_tokens == 0) return MOE_OK;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  uint32_t* flags = at<uint32_t>(ws, L.flags);
+  MOE_HIP(launch_clear_flags(flags, st));
+  const bool split = L.ksplit > 1;
+  void* dst = split ? at<void>(ws, L.y) : y_perm;
+  MOE_TRY(run_ffn_i8(s, x_codes, nullptr, x_scales, expert_offsets, *experts, split ? MOE_F32 : y_dtype, dst, ws, L,
+                     st, nullptr, L.ksplit));
+  const int slots = s.num_tokens * s.top_k;
+  if (split)
+    MOE_HIP(launch_sum_parts(at<float>(ws, L.y), L.ksplit, (long long)slots * s.hidden, s.hidden,
+                             expert_offsets + s.num_experts, slots, y_dtype, y_perm, flags, st));
+  return MOE_OK;
+}
+
+moe_status moe_norm(int32_t rows, int32_t cols, int32_t src_dtype, const void* x, const float* weight, float eps,
+                    int32_t out_dtype, void* out, int8_t* codes, float* scales, void* stream) {
+  if (rows < 0 || cols <= 0 || !is_stream_type(src_dtype)) return MOE_ERR_INVALID_ARG;
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  if (!out && !codes) return MOE_ERR_INVALID_ARG;
+  if ((codes == nullptr) != (scales == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (out && !is_stream_type(out_dtype)) return MOE_ERR_INVALID_ARG;
+  const bool f32 = src_dtype == MOE_F32 && (!out || out_dtype == MOE_F32);
+  if (cols % (codes ? 128 : (f32 ? 4 : 64))) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(need(x));
+  MOE_TRY(opt16(weight));
+  MOE_TRY(opt16(out));
+  MOE_TRY(opt16(codes));
+  MOE_TRY(opt4(scales));
+  // in place the types have to be the same
+  if (out == x && out_dtype != src_dtype) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  MOE_HIP(launch_norm(rows, cols, src_dtype, x, weight, eps, out_dtype, out, codes, scales,
+                      static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_combine_norm(const moe_shape* shape, const moe_block* block, int32_t y_dtype, const void* y_perm,
+                            const int32_t* row_of_slot, const float* topk_gates, const void* y_shared,
+                            const void* residual, void* out, void* stream) {
+  MOE_TRY(check_shape(shape));
+  const moe_shape& s = *shape;
+  MOE_TRY(check_block_end(block));
+  if (!is_float_type(y_dtype)) return MOE_ERR_INVALID_ARG;
+  if (s.hidden % 8 && y_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(need(y_perm));
+  MOE_TRY(need4(row_of_slot));
+  MOE_TRY(need4(topk_gates));
+  MOE_TRY(opt16(y_shared));
+  MOE_TRY(opt16(residual));
+  if (!residual && block->residual_scale != 0.0f) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(out));
+  if (s.num_tokens == 0) return MOE_OK;
+  MOE_HIP(launch_combine_norm(s, *block, y_dtype, y_perm, row_of_slot, topk_gates, y_shared, residual, out,
+                              static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_workspace_size_block(const moe_shape* shape, size_t* bytes) {
+  MOE_TRY(check_shape(shape));
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = plan_workspace(*shape, kExpertsAct, true).total;
+  return MOE_OK;
+}
+
+moe_status moe_block_forward(const moe_shape* shape, const moe_block* block, const void* x, const void* w_router,
+                             const float* router_bias, const int32_t* k_per_token, const void* w_gate,
+                             const void* w_up, const void* w_down, const void* ws_gate, const void* ws_up,
+                             const void* ws_down, void* out, const moe_debug* dbg, void* ws, size_t ws_bytes,
+                             void* stream) {
+  MOE_TRY(check_shape(shape));
+  const moe_shape& s = *shape;
+  MOE_TRY(check_block_args(s, block, x, w_router, router_bias, k_per_token, out, dbg));
+  const void* const wt[6] = {w_gate, w_up, w_down, ws_gate, ws_up, ws_down};
+  for (int i = 0; i < (s.shared_intermediate > 0 ? 6 : 3); ++i) MOE_TRY(need(wt[i]));
+  MOE_TRY(need(ws));
+  const WsLayout L = plan_workspace(s, kExpertsAct, true);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (s.num_tokens == 0) return MOE_OK;
+  return run_block(s, *block, x, w_router, router_bias, k_per_token, wt, nullptr, nullptr, out, dbg, ws, L,
+                   static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_block_forward_int8(const moe_shape* shape, const moe_block* block, const void* x,
+                                  const void* w_router, const float* router_bias, const int32_t* k_per_token,
+                                  const moe_int8_ffn* experts, const moe_int8_ffn* shared, void* out,
+                                  const moe_debug* dbg, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_int8_shape(shape));
+  const moe_shape& s = *shape;
+  MOE_TRY(check_block_args(s, block, x, w_router, router_bias, k_per_token, out, dbg));
+  MOE_TRY(check_int8_ffn(experts));
+  if (s.shared_intermediate > 0) MOE_TRY(check_int8_ffn(shared));
+  MOE_TRY(need(ws));
+  const WsLayout L = plan_workspace(s, kExpertsI8, true);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (s.num_tokens == 0) return MOE_OK;
+  return run_block(s, *block, x, w_router, router_bias, k_per_token, nullptr, experts, shared, out, dbg, ws, L,
+                   static_cast<hipStream_t>(stream));
 }
 
 moe_status moe_group_score_sigmoid(const float* x, float* y, int64_t n, void* stream) {

@@ -26,9 +26,12 @@ struct MTile {
 // MXFP8 layers add the quantised x (xq, scales xsc with stride T, and the
 // same scales in dispatch-row order, xscp with stride T*top_k) and the scales
 // of h (hsc, stride T*top_k) and of the shared expert's h (hssc, stride T);
-// h and hs then hold one-byte codes.
+// h and hs then hold one-byte codes.  Int8 layers keep h and hs in fp16 and
+// add their codes (hq, hsq: the hq region serves both) and the fp32 row scales
+// of x (xsc), h (hsc) and hs (hssc).  Block calls with a norm in front add the
+// normed x (xn).
 struct WsLayout {
-  size_t flags, logits, logits_parts, ids, gates, counts, offsets, tile_counts, row_of_slot, row_token,
+  size_t xn, hq, flags, logits, logits_parts, ids, gates, counts, offsets, tile_counts, row_of_slot, row_token,
       num_dropped, sched_big, sched_small, sched_count, h, y, hs, ys, xq, xsc, xscp, hsc, hssc, gu_parts,
       ep_tile_counts, total;
   int n_dispatch_tiles;
@@ -72,7 +75,10 @@ struct GemmPlan {
 };
 
 GemmPlan choose_gemm_plan(const moe_shape& s);
-WsLayout plan_workspace(const moe_shape& s, bool mx = false);
+// number format of the experts
+enum ExpertFormat { kExpertsAct = 0, kExpertsMX = 1, kExpertsI8 = 2 };
+// normed: the call also keeps a normed copy of x
+WsLayout plan_workspace(const moe_shape& s, int format = kExpertsAct, bool normed = false);
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -212,6 +218,61 @@ hipError_t launch_gemm_down_mx2(const void* A, const uint8_t* hsc, int hs_stride
 
 // Row-tile height the GEMM launchers use for a dtype and a requested height.
 int gemm_tile_rows(int dtype, int bm_hint);
+
+// ---- int8 operands (gemm.hip, int8.hip) ----------------------------------------
+// Token codes A with one fp32 scale per row (sa; gathered through a_rows with
+// the rows), weight codes with one per output channel (sb*, expert e's start at
+// e * N), int32 sums.  K a multiple of 128, N of 16, bm 256, 128 or 32.
+hipError_t launch_gemm_gateup_i8(int bm, const void* A, const int32_t* a_rows, const float* sa, const void* Bg,
+                                 const float* sbg, const void* Bu, const float* sbu, int N, int K, void* h,
+                                 const MTile* sched, const int32_t* count, int max_tiles, int static_rows,
+                                 uint32_t* flags, hipStream_t st);
+// the int32 gate and up sums of ksplit ranges of K (32-row tiles): range p's at
+// parts + p * part_elems and parts + (ksplit + p) * part_elems
+hipError_t launch_gemm_gateup_i8_parts(const void* A, const int32_t* a_rows, const void* Bg, const void* Bu, int N,
+                                       int K, int32_t* parts, const MTile* sched, const int32_t* count,
+                                       int max_tiles, int static_rows, int ksplit, long long part_elems,
+                                       hipStream_t st);
+// y = sa sb A.B^T in y_dtype; ksplit > 1 (fp32): K in ksplit ranges, range p's
+// share at Y + p * part_elems
+hipError_t launch_gemm_down_i8(int bm, const void* A, const float* sa, const void* B, const float* sb, int N, int K,
+                               int y_dtype, void* Y, const MTile* sched, const int32_t* count, int max_tiles,
+                               int static_rows, uint32_t* flags, hipStream_t st, int ksplit = 1,
+                               long long part_elems = 0);
+// both row-tile classes in one interleaved launch
+hipError_t launch_gemm_gateup_i8_2(const void* A, const int32_t* a_rows, const float* sa, const void* Bg,
+                                   const float* sbg, const void* Bu, const float* sbu, int N, int K, void* h,
+                                   const MTile* sb, const int32_t* cb, int mb, const MTile* ss, const int32_t* cs,
+                                   int ms, uint32_t* flags, hipStream_t st);
+hipError_t launch_gemm_down_i8_2(const void* A, const float* sa, const void* B, const float* sb_w, int N, int K,
+                                 int y_dtype, void* Y, const MTile* sb, const int32_t* cb, int mb, const MTile* ss,
+                                 const int32_t* cs, int ms, uint32_t* flags, hipStream_t st, int ksplit = 1,
+                                 long long part_elems = 0);
+// rows of src (bf16, fp32 or fp16) to int8 codes and a scale per row; rows at
+// and beyond *rows_dev (nullable) are left alone
+hipError_t launch_quant_int8(int src_dtype, const void* src, int rows, int cols, const int32_t* rows_dev, void* codes,
+                             float* scales, hipStream_t st);
+// h = fp16(silu(g) u) from int32 partial sums (see launch_gemm_gateup_i8_parts)
+hipError_t launch_swiglu_parts_i8(const int32_t* parts, int nparts, long long part_elems, int N,
+                                  const int32_t* a_rows, const float* sa, const float* sbg, const float* sbu,
+                                  const MTile* sched, const int32_t* count, int max_tiles, int static_rows,
+                                  void* h, uint32_t* flags, hipStream_t st);
+// y = the sum of nparts partial sums in order, in y_dtype
+hipError_t launch_sum_parts(const float* parts, int nparts, long long part_elems, int N, const int32_t* rows_dev,
+                            int max_rows, int y_dtype, void* y, uint32_t* flags, hipStream_t st);
+
+// ---- norms around the layer (block.hip) ------------------------------------------
+hipError_t launch_norm(int rows, int cols, int src_dtype, const void* x, const float* weight, float eps,
+                       int out_dtype, void* out, void* codes, float* scales, hipStream_t st);
+hipError_t launch_combine_norm(const moe_shape& s, const moe_block& b, int y_dtype, const void* y,
+                               const int32_t* row_of_slot, const float* gates, const void* y_shared,
+                               const void* residual, void* out, hipStream_t st, int parts = 1,
+                               long long part_stride = 0);
+
+// ---- routing with a balance bias (route_biased.hip) --------------------------------
+hipError_t launch_route_biased(const moe_shape& s, const float* logits, const float* select_bias,
+                               const int32_t* k_per_token, int32_t* ids, float* gates, uint32_t* flags,
+                               hipStream_t st, int parts = 1, long long part_stride = 0, float* sum_out = nullptr);
 
 // ---- expert-parallel exchange over G virtual ranks (ep.hip) -----------------
 constexpr int kMaxRanks = 64;

@@ -1,0 +1,21 @@
+// silu(g) * u for the int8 experts, whose h decides 8-bit codes.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+namespace moe {
+
+// silu(g) = g / (1 + e^-g).  The rounding of -g * log2 e is carried into the
+// exponential (without it the result is off by |g| roundings, with it by one
+// or two), and the reciprocal is the hardware's, about one rounding.
+__device__ __forceinline__ float silu_mul_exact(float g, float u) {
+  const float a = -1.442695041f * g;
+  // log2 e = fp32(1.442695041) + 1.92596e-8
+  const float lo = fmaf(-1.442695041f, g, -a) + -1.92596e-8f * g;
+  const float e = __builtin_amdgcn_exp2f(a);
+  const float d = 1.0f + fmaf(e, 0.69314718f * lo, e);
+  // e = inf (g < -88): the reciprocal of inf is 0 and the result a zero
+  return g * __builtin_amdgcn_rcpf(e < 3.0e38f ? d : __builtin_inff()) * u;
+}
+
+}  // namespace moe

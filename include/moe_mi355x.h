@@ -405,6 +405,152 @@ moe_status moe_layer_forward_mxfp8(const moe_shape* shape, const void* x, const 
                                    void* out, const moe_debug* dbg, void* ws, size_t ws_bytes,
                                    void* stream);
 
+/* ---- routing with a balance bias ---------------------------------------
+ * A bias per expert that evens the experts' load without touching the model's
+ * mixture: it decides which experts a token takes, not how they are weighted
+ * (router_bias of moe_route_topk, a part of the logits, does both).  The
+ * server raises the bias of an idle expert and lowers that of a busy one
+ * between batches; -inf takes an expert out of service.
+ * Per token t with logits l (as moe_route_topk computes or takes them):
+ *   expert e is available when select_bias[e] > -inf and l[e] is not NaN;
+ *   infinite logits count as the largest finite ones;
+ *   score s[e]: sigmoid(l[e]), or the softmax of l over the available experts;
+ *   key = s[e] + select_bias[e];
+ *   with num_groups > 1 the eligible experts are those of the topk_groups
+ *   groups with the largest group score, the sum of the group's group_topn
+ *   (0: 1) largest keys (of all its available experts when it has fewer);
+ *   equal scores go to the lower group, a group without one is never kept;
+ *   selection: the k_t available eligible experts with the largest keys,
+ *   equal keys to the lower expert, in slots 0.. in that order; slots without
+ *   an expert get id -1 and gate 0;
+ *   gates: s of the selected experts, divided by their sum when renormalize
+ *   (for a sum of 0, gates of 0), times routed_scale.
+ * Keys, group scores and gates are computed in fp64, so the choice depends on
+ * no rounding in practice; gates are rounded once.  select_bias [E] fp32; the
+ * other arguments as for moe_route_topk.  Clears the workspace flag word. */
+moe_status moe_route_biased(const moe_shape* shape, const void* x, const void* w_router,
+                            const float* router_bias, const float* select_bias, const float* logits_in,
+                            float* logits_out, const int32_t* k_per_token, int32_t* topk_ids,
+                            float* topk_gates, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- int8 experts ------------------------------------------------------
+ * Symmetric 8-bit integers with one fp32 scale per token row and one per
+ * output channel of a weight (per weight row, as weights are output-major):
+ *   scale = amax / 127, code = 127 v / amax rounded to nearest, ties to even
+ *   (a row of zeros has scale 0 and codes 0);
+ *   y[r][n] = scale_a[r] * scale_b[n] * sum_k code_a[r][k] * code_b[n][k],
+ *   the sum exact in int32.
+ * K is a multiple of 128 and at most 131072, N a multiple of 16 (the calls
+ * with a shape: H, I and Is multiples of 128), act_dtype MOE_BF16. */
+
+/* Quantises src [rows][cols] (MOE_BF16, MOE_F32 or MOE_F16; cols a multiple
+ * of 128) to codes [rows][cols] and scales [rows].  Weights are quantised once
+ * with this call (rows = E*I or E*H).  Inputs are assumed finite (a row with an
+ * infinity or NaN gets unspecified codes). */
+moe_status moe_quantize_int8(int32_t rows, int32_t cols, int32_t src_dtype, const void* src, int8_t* codes,
+                             float* scales, void* stream);
+
+/* Grouped product: for every expert e and row r in [expert_offsets[e],
+ * expert_offsets[e+1]), y[r] = a[r] . b[e]^T as above, in y_dtype (MOE_F32,
+ * MOE_F16 or MOE_BF16).  a [rows][k] codes, b [num_experts][n][k] codes with
+ * scales [num_experts][n], y [rows][n].  expert_offsets [num_experts + 1] as
+ * moe_dispatch writes them, expert_offsets[num_experts] <= rows; NULL with
+ * num_experts == 1 for all rows.  Rows at or beyond
+ * expert_offsets[num_experts] are neither read nor written.  An fp16 y out of
+ * range sets MOE_FLAG_Y_RANGE in the workspace flag word (and is infinite). */
+moe_status moe_workspace_size_gemm_int8(int32_t rows, int32_t n, int32_t k, int32_t num_experts, size_t* bytes);
+moe_status moe_grouped_gemm_int8(int32_t rows, int32_t n, int32_t k, int32_t num_experts, const int8_t* a,
+                                 const float* a_scales, const int32_t* expert_offsets, const int8_t* b,
+                                 const float* b_scales, int32_t y_dtype, void* y, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+typedef struct {
+  const int8_t* gate;        /* [E][I][H] codes  */
+  const float* gate_scales;  /* [E][I]           */
+  const int8_t* up;          /* [E][I][H] codes  */
+  const float* up_scales;    /* [E][I]           */
+  const int8_t* down;        /* [E][H][I] codes  */
+  const float* down_scales;  /* [E][H]           */
+} moe_int8_ffn;
+/* The shared expert uses the same struct with E = 1. */
+
+/* Workspace of moe_grouped_ffn_int8 and moe_block_forward_int8. */
+moe_status moe_workspace_size_int8(const moe_shape* shape, size_t* bytes);
+
+/* S7-S8 with int8 operands: as moe_grouped_ffn, with x_perm given as codes
+ * [T*top_k][H] and scales [T*top_k]; h = silu(a) * u (fp32) is rounded to fp16
+ * -- values outside its range are clamped to it and set MOE_FLAG_H_RANGE -- and
+ * quantised per row before the down projection; y_perm in y_dtype (MOE_F32, or
+ * MOE_F16 or MOE_BF16; an fp16 value out of range sets MOE_FLAG_Y_RANGE).
+ * Clears the workspace flag word. */
+moe_status moe_grouped_ffn_int8(const moe_shape* shape, const int8_t* x_codes, const float* x_scales,
+                                const int32_t* expert_offsets, const moe_int8_ffn* experts, int32_t y_dtype,
+                                void* y_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- the block around the layer ----------------------------------------
+ * A transformer block's FFN half with the layer in it:
+ *   n = norm(x; pre_norm),  y = layer(n),
+ *   out = residual_scale * x + gate * norm(y; post_norm),
+ *   norm(v; w) = v / sqrt(mean(v^2) + eps) * w   (over the H columns).
+ * Sums and products in fp32, one rounding on each output. */
+typedef struct {
+  const float* select_bias;  /* [E]: routing as moe_route_biased; NULL: as moe_route_topk      */
+  const float* pre_norm;     /* [H] fp32; NULL: the layer takes x itself                       */
+  const float* post_norm;    /* [H] fp32; NULL: y is not normed                                */
+  float eps;                 /* > 0, both norms                                                */
+  float residual_scale;      /* finite; 0: x is not added                                      */
+  const void* gate;          /* gate value of token t, column c at element
+                                t * gate_row_stride + c * gate_col_stride; NULL: 1             */
+  int64_t gate_row_stride;   /* >= 0; 0: the same for all tokens                               */
+  int32_t gate_col_stride;   /* 0 (one value per token) or 1                                   */
+  int32_t gate_dtype;        /* MOE_F32 or MOE_BF16                                            */
+  int32_t stream_dtype;      /* MOE_F32 or MOE_BF16: x (the residual stream) and out           */
+} moe_block;
+/* The gate is 4-byte (fp32) or 2-byte (bf16) aligned; with column stride 1 its
+ * rows may start anywhere at that alignment. */
+
+/* The norm in front of the layer, with the quantisation the int8 experts want:
+ * n = norm(x) of rows [rows][cols] (src_dtype MOE_F32 or MOE_BF16; cols a
+ * multiple of 64, of 4 when src and out are fp32, of 128 with codes); out
+ * (nullable) in out_dtype (MOE_F32 or MOE_BF16); codes and scales (both or
+ * neither) quantise the unrounded n as moe_quantize_int8 does.  weight [cols]
+ * fp32 or NULL (1).  out may be x itself when the types are the same. */
+moe_status moe_norm(int32_t rows, int32_t cols, int32_t src_dtype, const void* x, const float* weight, float eps,
+                    int32_t out_dtype, void* out, int8_t* codes, float* scales, void* stream);
+
+/* S10 with the end of the block: y = the sum moe_combine forms (y_perm and
+ * y_shared in y_dtype: MOE_F32, MOE_F16 or MOE_BF16; a token without a kept
+ * slot has y_shared[t] or 0), out = residual_scale * residual + gate *
+ * norm(y; post_norm) in stream_dtype.  residual (stream_dtype) may be NULL only
+ * when residual_scale is 0, and may be out itself.  Of `block`, select_bias and
+ * pre_norm are not used.  H a multiple of 8 unless y_dtype and stream_dtype are
+ * MOE_F32. */
+moe_status moe_combine_norm(const moe_shape* shape, const moe_block* block, int32_t y_dtype, const void* y_perm,
+                            const int32_t* row_of_slot, const float* topk_gates, const void* y_shared,
+                            const void* residual, void* out, void* stream);
+
+/* The block in one call: moe_norm, routing (moe_route_biased with a
+ * select_bias, else moe_route_topk), moe_dispatch, moe_grouped_ffn,
+ * moe_combine_norm.  x and out [T][H] in block->stream_dtype (which has to be
+ * act_dtype when pre_norm is NULL); out may be x itself.  shape->out_dtype is
+ * not used.  The other arguments as for moe_layer_forward; `dbg` stages: the
+ * norm in front is outside every stage.  moe_workspace_size_block gives the
+ * workspace. */
+moe_status moe_workspace_size_block(const moe_shape* shape, size_t* bytes);
+moe_status moe_block_forward(const moe_shape* shape, const moe_block* block, const void* x, const void* w_router,
+                             const float* router_bias, const int32_t* k_per_token, const void* w_gate,
+                             const void* w_up, const void* w_down, const void* ws_gate, const void* ws_up,
+                             const void* ws_down, void* out, const moe_debug* dbg, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* The same with int8 experts and, when shape->shared_intermediate > 0, an int8
+ * shared expert: the norm in front also quantises its rows (without one, x is
+ * quantised: the gather stage). */
+moe_status moe_block_forward_int8(const moe_shape* shape, const moe_block* block, const void* x,
+                                  const void* w_router, const float* router_bias, const int32_t* k_per_token,
+                                  const moe_int8_ffn* experts, const moe_int8_ffn* shared, void* out,
+                                  const moe_debug* dbg, void* ws, size_t ws_bytes, void* stream);
+
 /* The fp32 logistic function that group-limited routing sums into group
  * scores, evaluated elementwise: y[i] = sigma(x[i]) for i < n (device
  * arrays).  Node-limited routing ("Expert parallelism for MoE serving",

@@ -1,0 +1,175 @@
+"""Routing with a balance bias against the plain 64-bit form: the choice exact, gates within one rounding to fp32
+(2^-24 relative, and 1e-13 for the 64-bit steps before it)."""
+
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+from expert_serving_amd import abi
+
+import plain_block as P
+from gpu_util import dev, f32, i32, say, workspace
+
+pytestmark = pytest.mark.gpu
+NEG = -np.inf
+
+
+def shape_of(T, E, k, o):
+    return abi.make_shape(num_tokens=T, hidden=64, num_experts=E, intermediate=64, top_k=k,
+                          score=int(o.get("score", "sigmoid") == "sigmoid"), renormalize=int(o.get("renorm", True)),
+                          routed_scale=o.get("scale", 1.0), num_groups=o.get("G", 1), topk_groups=o.get("keep", 1),
+                          group_topn=o.get("topn", 0))
+
+
+def route(logits, bias, k, kpt=None, **o):
+    T, E = logits.shape
+    s = shape_of(T, E, k, o)
+    ids, gates, ws = i32(T * k, -7).view(T, k), f32((T, k)).fill_(-7.0), workspace(s)
+    kd = None if kpt is None else torch.from_numpy(np.asarray(kpt, np.int32)).to(dev())
+    abi.moe_route_biased(s, None, None, None, torch.from_numpy(bias).to(dev()), torch.from_numpy(logits).to(dev()),
+                         None, kd, ids, gates, ws)
+    torch.cuda.synchronize()
+    return ids.cpu().numpy(), gates.cpu().numpy(), abi.moe_read_device_flags(ws)
+
+
+def check(logits, bias, k, kpt=None, **o):
+    logits, bias = np.ascontiguousarray(logits, np.float32), np.ascontiguousarray(bias, np.float32)
+    ids, gates, flags = route(logits, bias, k, kpt, **o)
+    want, w = P.route_biased(logits, bias, k, kpt, **o)
+    assert np.array_equal(ids, want), np.nonzero((ids != want).any(1))[0][:5]
+    assert np.all(np.abs(gates - w) <= (P.U32 + 1e-13) * np.abs(w) + 1e-45)
+    return ids, gates, flags
+
+
+CASES = {
+    "one_token_groups": (1, 256, 8, dict(G=8, keep=4, topn=2, scale=2.5)),
+    "groups_256": (1003, 256, 8, dict(G=8, keep=4, topn=2, scale=2.5)),
+    "groups_512_topn8": (67, 512, 16, dict(G=4, keep=2, topn=8)),
+    "groups_lds": (130, 72, 6, dict(G=6, keep=3, topn=3)),
+    "groups_lds_64": (31, 448, 5, dict(G=64, keep=20, topn=2, score="softmax")),
+    "groups_of_one": (33, 60, 4, dict(G=60, keep=7)),
+    "groups_all_kept": (40, 96, 8, dict(G=3, keep=3, topn=1, score="softmax")),
+    "softmax": (515, 128, 8, dict(score="softmax")),
+    "softmax_plain_gates": (100, 511, 3, dict(score="softmax", renorm=False, scale=2.0)),
+    "sigmoid_plain_gates": (100, 65, 1, dict(renorm=False)),
+    "all_experts": (9, 8, 8, dict()),
+    "one_expert": (5, 1, 1, dict(score="softmax")),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_choice_and_gates(name):
+    T, E, k, o = CASES[name]
+    say(f"route_biased {name}")
+    r = np.random.default_rng(len(name) * 1000 + E)
+    logits = r.normal(size=(T, E)) * 2
+    bias = r.normal(size=E) * (0.2 if o.get("score", "sigmoid") == "sigmoid" else 0.5 / E)
+    check(logits, bias, k, **o)
+
+
+@pytest.mark.parametrize("score,G", [("sigmoid", 1), ("softmax", 1), ("sigmoid", 4)])
+def test_equal_keys_go_to_the_lower_expert(score, G):
+    r = np.random.default_rng(5)
+    logits, bias = r.normal(size=(200, 64)).astype(np.float32), (r.normal(size=64) * 0.1).astype(np.float32)
+    logits[:, 32:] = logits[:, :32]           # experts e and e + 32 tie in every token
+    bias[32:] = bias[:32]
+    logits[::7] = 0.25                        # and here whole rows do
+    ids, _, _ = check(logits, bias, 8, score=score, G=G, keep=max(1, G // 2), topn=2)
+    bias[:] = 0
+    ids, _, _ = check(logits, bias, 8, score=score, G=G, keep=max(1, G // 2), topn=2)
+    if G == 1:
+        assert np.array_equal(ids[0], np.arange(8))
+
+
+def test_saturated_scores_keep_their_order():
+    """Logits 16 to 23: one fp32 sigmoid, eight different scores; the choice follows the logit."""
+    logits = np.tile(np.arange(16, 24, dtype=np.float32), (3, 1))
+    ids, _, _ = check(logits, np.zeros(8), 4)
+    assert np.array_equal(ids[0], [7, 6, 5, 4])
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_experts_out_of_service_nan_and_infinite_logits(score):
+    r = np.random.default_rng(9)
+    logits, bias = r.normal(size=(120, 40)).astype(np.float32), np.zeros(40, np.float32)
+    bias[[3, 17, 39]] = NEG
+    bias[8] = np.nan
+    logits[:, 17] = np.nan                    # a masked place may hold anything
+    logits[:, 39] = np.inf
+    logits[5, :] = np.nan                     # nothing left
+    logits[6, 1:] = np.nan                    # one expert left
+    logits[7, 4], logits[8, 4], logits[9, 4] = np.inf, -np.inf, np.nan
+    logits[10, :] = -np.inf
+    logits[11, 0:20] = np.inf
+    logits[12, :] = -3.0e38
+    ids, gates, _ = check(logits, bias, 6, score=score)
+    assert (ids[5] == -1).all() and (gates[5] == 0).all() and (ids[6][1:] == -1).all()
+    assert not np.isin(ids, [3, 8, 17, 39]).any() and np.isfinite(gates).all()
+    check(logits, bias, 6, score=score, G=4, keep=2, topn=2)
+    bias[:] = NEG
+    ids, gates, _ = check(logits, bias, 6, score=score)
+    assert (ids == -1).all() and (gates == 0).all()
+    bias[:] = 0
+    bias[[2, 30]] = np.inf                    # forced into every token
+    ids, _, _ = check(logits[:5], bias, 6, score=score)
+    assert (ids[:, 0] == 2).all() and (ids[:, 1] == 30).all()
+
+
+def test_groups_with_few_available_experts():
+    r = np.random.default_rng(11)
+    logits, bias = r.normal(size=(64, 32)).astype(np.float32), np.zeros(32, np.float32)
+    bias[0:8] = NEG                           # group 0 has none
+    bias[9:16] = NEG                          # group 1 has one
+    ids, _, _ = check(logits, bias, 5, G=4, keep=3, topn=3)
+    assert not (ids == 0).any()
+    bias[16:32] = NEG                         # one expert in all
+    ids, _, _ = check(logits, bias, 5, G=4, keep=3, topn=3)
+    assert (ids[:, 0] == 8).all() and (ids[:, 1:] == -1).all()
+
+
+def test_gates_of_scores_that_vanish():
+    logits = np.full((2, 4), -3.0e38, np.float32)
+    _, gates, _ = check(logits, np.zeros(4), 2)            # sigmoid 0 everywhere: gates of 0
+    assert (gates == 0).all()
+
+
+def test_k_per_token_and_bad_k():
+    r = np.random.default_rng(3)
+    logits, bias = r.normal(size=(300, 128)), r.normal(size=128) * 0.1
+    kpt = r.integers(1, 9, 300)
+    _, _, flags = check(logits, bias, 8, kpt)
+    assert flags == 0
+    kpt[[0, 4, 299]] = [0, 9, -3]
+    _, _, flags = check(logits, bias, 8, kpt)
+    assert flags == abi.MOE_FLAG_BAD_K
+
+
+@pytest.mark.parametrize("T,E,H", [(5, 16, 512), (40, 64, 1024), (2048, 128, 1024), (2049, 256, 2048)])
+def test_from_activations(T, E, H):
+    """With x and a router: the choice on the logits it reports (the last two sizes split the router's K)."""
+    k = 4
+    x = W.normal((T, H), 1.0, W.DT_BF16, dev(), 1)
+    wr = W.normal((E, H), H ** -0.5, W.DT_BF16, dev(), 2)
+    rb = W.normal((E,), 0.3, W.DT_F32, dev(), 3)
+    bias = W.normal((E,), 0.1, W.DT_F32, dev(), 4)
+    s = abi.make_shape(num_tokens=T, hidden=H, num_experts=E, intermediate=64, top_k=k, score=1)
+    ids, gates, lo, ws = i32((T, k)), f32((T, k)), f32((T, E)), workspace(s)
+    abi.moe_route_biased(s, x, wr, rb, bias, None, lo, None, ids, gates, ws)
+    torch.cuda.synchronize()
+    own = x.double().cpu() @ wr.double().cpu().t() + rb.double().cpu()
+    assert (lo.double().cpu() - own).abs().max() <= 1e-5 * own.square().mean().sqrt()
+    n = min(T, 300)
+    want, w = P.route_biased(lo[:n].cpu().numpy(), bias.cpu().numpy(), k)
+    assert np.array_equal(ids[:n].cpu().numpy(), want)
+    assert np.all(np.abs(gates[:n].cpu().numpy() - w) <= (P.U32 + 1e-13) * w)
+
+
+def test_a_zero_bias_is_the_plain_router():
+    """Bias 0, one group: the ids of moe_route_topk (gates too, to two roundings of its fp32 steps)."""
+    lg = W.make_logits(700, 128, dev(), seed=8, tie_fraction=0.1)
+    s = abi.make_shape(num_tokens=700, hidden=64, num_experts=128, intermediate=64, top_k=6)
+    a, b, ga, gb, ws = i32((700, 6)), i32((700, 6)), f32((700, 6)), f32((700, 6)), workspace(s)
+    abi.moe_route_topk(s, None, None, None, lg, None, None, a, ga, ws)
+    abi.moe_route_biased(s, None, None, None, torch.zeros(128, device=dev()), lg, None, None, b, gb, ws)
+    assert torch.equal(a, b) and torch.allclose(ga, gb, rtol=1e-6, atol=0)
