@@ -165,11 +165,19 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_current = None  # () -> the current device's current stream, without the stream object torch would make
+
+
 def _stream(stream):
+    global _current
     if stream is not None:
         return stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    if _current is None:
+        import torch
+        torch.cuda.init()
+        raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        _current = (lambda: raw(dev())) if raw and dev else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _current()
 
 
 def _check(status: int, where: str):

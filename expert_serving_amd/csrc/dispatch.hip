@@ -336,9 +336,11 @@ __global__ __launch_bounds__(512) void k_build_sched(const int32_t* __restrict__
                                                      int tail_rows,
                                                      MTile* __restrict__ sched_big, int max_big,
                                                      MTile* __restrict__ sched_small, int max_small,
-                                                     int32_t* __restrict__ count) {
+                                                     int32_t* __restrict__ count,
+                                                     uint32_t* __restrict__ flags) {
   __shared__ int s_big[512], s_small[512];
   const int tid = threadIdx.x;
+  if (flags && tid == 0) *flags = 0u;
   // an expert with at least split_rows rows takes big tiles; smaller experts
   // take small tiles only.  A remainder of at most tail_rows rows past a big
   // expert's last full tile goes to small tiles too: a big tile would cost
@@ -492,10 +494,10 @@ hipError_t launch_gather(const moe_shape& s, const void* x, const int32_t* row_t
 
 hipError_t launch_build_schedule(const int32_t* offsets, int E, const GemmPlan& plan,
                                  MTile* sched_big, int max_big, MTile* sched_small, int max_small,
-                                 int32_t* count, hipStream_t st) {
+                                 int32_t* count, hipStream_t st, uint32_t* flags) {
   hipLaunchKernelGGL(k_build_sched, dim3(1), dim3(512), 0, st, offsets, E, plan.bm_big,
                      plan.bm_small, plan.split_rows, plan.tail_rows, sched_big, max_big, sched_small,
-                     max_small, count);
+                     max_small, count, flags);
   return hipGetLastError();
 }
 

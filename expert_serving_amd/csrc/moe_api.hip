@@ -324,6 +324,22 @@ int gate_up_parts(long long blocks, int stages, bool rounds) {
   return best;
 }
 
+// int8 products of small row tiles stream their weights (launch_stream_i8)
+// while `weight_bytes`, what the batch's experts hold at most, stays below this;
+// above it the LDS tiles come nearer to the memory's rate.
+constexpr long long kStreamMaxBytes = 160LL << 20;
+bool stream_i8(const GemmPlan& gp, const moe_shape& s, long long matrix_bytes) {
+  const long long slots = (long long)s.num_tokens * s.top_k;
+  return !gp.has_big() && std::min<long long>(slots, s.num_experts) * matrix_bytes <= kStreamMaxBytes;
+}
+
+// Row tiles of a plan without big tiles: each expert that has rows ends with
+// one tile that may be short.
+int stream_tiles(const moe_shape& s, int max_small) {
+  const long long slots = (long long)s.num_tokens * s.top_k;
+  return (int)std::min<long long>(max_small, std::min<long long>(slots, s.num_experts) + slots / 32);
+}
+
 }  // namespace
 
 WsLayout plan_workspace(const moe_shape& s, int format, bool normed) {
@@ -348,6 +364,13 @@ WsLayout plan_workspace(const moe_shape& s, int format, bool normed) {
     // the shared expert of a few tokens (32-row tiles below 128 tokens)
     if (Is > 0 && T < 128)
       w.ks_gus = gate_up_parts((long long)((T + 31) / 32) * (long long)((Is + 255) / 256), stages, false);
+  }
+  if (i8) {
+    w.stream = stream_i8(gp, s, 3LL * (long long)(H * I));
+    // the shared expert: a batch whose every row takes one expert
+    w.stream_shared = Is > 0 && T < 64 && 3LL * (long long)(H * Is) <= kStreamMaxBytes;
+    if (w.stream) w.ksplit = w.ks_gu = 1;
+    if (w.stream_shared) w.ks_gus = 1;
   }
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -601,7 +624,7 @@ moe_status run_shared(const moe_shape& s, const void* x, const void* wsg, const 
 // With y_dtype fp32 and ksplit > 1, y holds ksplit partial sums.
 moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows, const float* xsc,
                       const int32_t* offsets, const moe_int8_ffn& w, int y_dtype, void* y, void* ws,
-                      const WsLayout& L, hipStream_t st, const moe_debug* dbg, int ksplit) {
+                      const WsLayout& L, hipStream_t st, const moe_debug* dbg, int ksplit, bool clear_flags) {
   const GemmPlan gp = choose_gemm_plan(s);
   const int E = s.num_experts, H = s.hidden, I = s.intermediate;
   const int slots = s.num_tokens * s.top_k;
@@ -613,9 +636,14 @@ moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows,
   void* hq = at<void>(ws, L.hq);
   float* hsc = at<float>(ws, L.hsc);
   const bool merged = gp.has_big() && gp.has_small();
-  MOE_HIP(launch_build_schedule(offsets, E, gp, sb, L.max_tiles_big, ss, L.max_tiles_small, cnt, st));
+  const int tiles = stream_tiles(s, L.max_tiles_small);
+  MOE_HIP(launch_build_schedule(offsets, E, gp, sb, L.max_tiles_big, ss, L.max_tiles_small, cnt, st,
+                                clear_flags ? flags : nullptr));
   MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, true, st));
-  if (merged) {
+  if (L.stream) {
+    MOE_HIP(launch_stream_i8(xq, a_rows, xsc, w.gate, w.gate_scales, w.up, w.up_scales, I, H, 0, h, ss, cnt + 1, tiles,
+                             nullptr, 0, flags, st));
+  } else if (merged) {
     MOE_HIP(launch_gemm_gateup_i8_2(xq, a_rows, xsc, w.gate, w.gate_scales, w.up, w.up_scales, I, H, h, sb, cnt,
                                     L.max_tiles_big, ss, cnt + 1, L.max_tiles_small, flags, st));
   } else if (L.ks_gu > 1) {
@@ -633,7 +661,10 @@ moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows,
   MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, false, st));
   MOE_HIP(stage_mark(dbg, MOE_STAGE_DOWN, true, st));
   const long long pe = (long long)slots * H;
-  if (merged)
+  if (L.stream)
+    MOE_HIP(launch_stream_i8(hq, nullptr, hsc, w.down, w.down_scales, nullptr, nullptr, H, I, y_dtype, y, ss, cnt + 1,
+                             tiles, nullptr, 0, flags, st));
+  else if (merged)
     MOE_HIP(launch_gemm_down_i8_2(hq, hsc, w.down, w.down_scales, H, I, y_dtype, y, sb, cnt, L.max_tiles_big, ss,
                                   cnt + 1, L.max_tiles_small, flags, st, ksplit, pe));
   else
@@ -651,6 +682,14 @@ moe_status run_shared_i8(const moe_shape& s, const void* xq, const float* xsc, c
   void* hs = at<void>(ws, L.hs);
   float* hssc = at<float>(ws, L.hssc);
   uint32_t* flags = at<uint32_t>(ws, L.flags);
+  if (L.stream_shared) {
+    MOE_HIP(launch_stream_i8(xq, nullptr, xsc, w.gate, w.gate_scales, w.up, w.up_scales, Is, H, 0, hs, nullptr, nullptr,
+                             0, nullptr, T, flags, st));
+    MOE_HIP(launch_quant_int8(MOE_F16, hs, T, Is, nullptr, at<void>(ws, L.hq), hssc, st));
+    MOE_HIP(launch_stream_i8(at<void>(ws, L.hq), nullptr, hssc, w.down, w.down_scales, nullptr, nullptr, H, Is,
+                             y_dtype, at<void>(ws, L.ys), nullptr, nullptr, 0, nullptr, T, flags, st));
+    return MOE_OK;
+  }
   if (L.ks_gus > 1 && bm == 32) {
     int32_t* parts = at<int32_t>(ws, L.gu_parts);
     const long long pe = (long long)T * Is;
@@ -674,6 +713,7 @@ struct GemmI8Plan {
   moe_shape s;
   GemmPlan gp;
   int max_big, max_small, ksplit;
+  bool stream;
   size_t flags, sched_big, sched_small, sched_count, parts, total;
 };
 
@@ -688,7 +728,8 @@ GemmI8Plan plan_gemm_i8(int rows, int n, int k, int E) {
   p.s.act_dtype = MOE_BF16;
   p.gp = choose_gemm_plan(p.s);
   tile_bounds(p.s, p.gp, p.max_big, p.max_small);
-  p.ksplit = down_parts(p.s, p.gp, p.max_small, true);
+  p.stream = stream_i8(p.gp, p.s, (long long)n * k);
+  p.ksplit = p.stream ? 1 : down_parts(p.s, p.gp, p.max_small, true);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at_ = o;
@@ -867,7 +908,7 @@ moe_status run_block(const moe_shape& s, const moe_block& b, const void* x, cons
   float* sum_out = rparts > 1 ? logits : nullptr;
   const long long pstride = (long long)T * s.num_experts;
   if (b.select_bias)
-    MOE_HIP(launch_route_biased(s, lg, b.select_bias, k_per_token, ids, gates, flags, st, rparts, pstride, sum_out));
+    MOE_HIP(launch_route_biased(s, lg, b.select_bias, k_per_token, ids, gates, flags, false, st, rparts, pstride, sum_out));
   else
     MOE_HIP(launch_route_topk(s, lg, k_per_token, ids, gates, flags, st, rparts, pstride, sum_out));
   MOE_HIP(stage_mark(dbg, MOE_STAGE_ROUTE, false, st));
@@ -879,7 +920,7 @@ moe_status run_block(const moe_shape& s, const moe_block& b, const void* x, cons
   if (experts && !b.pre_norm) MOE_HIP(launch_quant_int8(MOE_BF16, x, T, H, nullptr, xq, xsc, st));
   MOE_HIP(stage_mark(dbg, MOE_STAGE_GATHER, false, st));
   if (experts)
-    MOE_TRY(run_ffn_i8(s, xq, row_token, xsc, offsets, *experts, y_dtype, y, ws, L, st, dbg, L.ksplit));
+    MOE_TRY(run_ffn_i8(s, xq, row_token, xsc, offsets, *experts, y_dtype, y, ws, L, st, dbg, L.ksplit, false));
   else
     MOE_TRY(run_ffn(s, xl, row_token, offsets, wt[0], wt[1], wt[2], y, ws, L, st, dbg, L.ksplit, y_half));
   const void* ys = nullptr;
@@ -1337,10 +1378,10 @@ moe_status moe_route_biased(const moe_shape* shape, const void* x, const void* w
     MOE_TRY(run_router(s, x, w_router, router_bias, lo, flags, st, pb, rparts));
     logits = rparts > 1 ? pb : lo;
     sum_out = rparts > 1 ? lo : nullptr;
-  } else {
-    MOE_HIP(launch_clear_flags(flags, st));
   }
-  MOE_HIP(launch_route_biased(s, logits, select_bias, k_per_token, topk_ids, topk_gates, flags, st, rparts,
+  const bool own = logits_in && (!k_per_token || s.num_tokens <= kRouteOwnFlagsTokens);
+  if (logits_in && !own) MOE_HIP(launch_clear_flags(flags, st));
+  MOE_HIP(launch_route_biased(s, logits, select_bias, k_per_token, topk_ids, topk_gates, flags, own, st, rparts,
                               (long long)s.num_tokens * s.num_experts, sum_out));
   return MOE_OK;
 }
@@ -1390,14 +1431,23 @@ moe_status moe_grouped_gemm_int8(int32_t rows, int32_t n, int32_t k, int32_t num
   const bool split = p.ksplit > 1;
   void* dst = split ? at<void>(ws, p.parts) : y;
   const int dt = split ? MOE_F32 : y_dtype;
-  MOE_HIP(launch_clear_flags(flags, st));
+  if (p.stream && num_experts == 1) {
+    MOE_HIP(launch_clear_flags(flags, st));
+    MOE_HIP(launch_stream_i8(a, nullptr, a_scales, b, b_scales, nullptr, nullptr, n, k, y_dtype, y, nullptr, nullptr, 0,
+                             expert_offsets ? expert_offsets + 1 : nullptr, rows, flags, st));
+    return MOE_OK;
+  }
   if (!expert_offsets) {
+    MOE_HIP(launch_clear_flags(flags, st));
     const int bm = rows >= 2048 ? 256 : (rows >= 128 ? 128 : 32);
     MOE_HIP(launch_gemm_down_i8(bm, a, a_scales, b, b_scales, n, k, dt, dst, nullptr, nullptr, 0, rows, flags, st,
                                 p.ksplit, pe));
   } else {
-    MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sb, p.max_big, ss, p.max_small, cnt, st));
-    if (p.gp.has_big() && p.gp.has_small())
+    MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sb, p.max_big, ss, p.max_small, cnt, st, flags));
+    if (p.stream)
+      MOE_HIP(launch_stream_i8(a, nullptr, a_scales, b, b_scales, nullptr, nullptr, n, k, y_dtype, y, ss, cnt + 1,
+                               stream_tiles(p.s, p.max_small), nullptr, 0, flags, st));
+    else if (p.gp.has_big() && p.gp.has_small())
       MOE_HIP(launch_gemm_down_i8_2(a, a_scales, b, b_scales, n, k, dt, dst, sb, cnt, p.max_big, ss, cnt + 1,
                                     p.max_small, flags, st, p.ksplit, pe));
     else
@@ -1434,11 +1484,10 @@ moe_status moe_grouped_ffn_int8(const moe_shape* shape, const int8_t* x_codes, c
   if (s.num_tokens == 0) return MOE_OK;
   hipStream_t st = static_cast<hipStream_t>(stream);
   uint32_t* flags = at<uint32_t>(ws, L.flags);
-  MOE_HIP(launch_clear_flags(flags, st));
   const bool split = L.ksplit > 1;
   void* dst = split ? at<void>(ws, L.y) : y_perm;
   MOE_TRY(run_ffn_i8(s, x_codes, nullptr, x_scales, expert_offsets, *experts, split ? MOE_F32 : y_dtype, dst, ws, L,
-                     st, nullptr, L.ksplit));
+                     st, nullptr, L.ksplit, true));
   const int slots = s.num_tokens * s.top_k;
   if (split)
     MOE_HIP(launch_sum_parts(at<float>(ws, L.y), L.ksplit, (long long)slots * s.hidden, s.hidden,

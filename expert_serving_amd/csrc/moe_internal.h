@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "moe_mi355x.h"
 
 namespace moe {
@@ -44,6 +46,9 @@ struct WsLayout {
   // partial gate and up sums in gu_parts, reduced by launch_swiglu_parts
   int ks_gu, ks_gus;
   int max_tiles_big, max_tiles_small;
+  // int8 layers: the routed and the shared expert's products run as streams
+  // of the weights (launch_stream_i8; then ksplit, ks_gu and ks_gus are 1)
+  bool stream, stream_shared;
 };
 
 // K from which the 32-row bf16 down tiles are 8-wave 32 x 256 blocks (else
@@ -82,6 +87,22 @@ WsLayout plan_workspace(const moe_shape& s, int format = kExpertsAct, bool norme
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+// Raises a kernel's dynamic LDS limit once per device when it exceeds the
+// default 64 KiB (setting it again is harmless, so concurrent first calls may
+// both set it).
+inline hipError_t allow_lds(const void* kernel, int lds, std::atomic<uint64_t>& set_on) {
+  if (lds <= 65536) return hipSuccess;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (set_on.load(std::memory_order_acquire) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
+  set_on.fetch_or(bit, std::memory_order_release);
+  return hipSuccess;
+}
+
 // ---- launchers (each returns the launch status) ----------------------------
 hipError_t launch_clear_flags(uint32_t* flags, hipStream_t st);
 
@@ -118,9 +139,10 @@ hipError_t launch_gather(const moe_shape& s, const void* x, const int32_t* row_t
                          const int32_t* offsets, void* x_perm, hipStream_t st);
 
 // Both tile lists (see GemmPlan); count[0] = big tiles, count[1] = small tiles.
+// flags (nullable) is cleared.
 hipError_t launch_build_schedule(const int32_t* offsets, int E, const GemmPlan& plan,
                                  MTile* sched_big, int max_big, MTile* sched_small, int max_small,
-                                 int32_t* count, hipStream_t st);
+                                 int32_t* count, hipStream_t st, uint32_t* flags = nullptr);
 
 // Grouped GEMMs.  `sched`/`count` give the row tiles; when sched == nullptr
 // the rows [0, static_rows) form one group (expert 0) tiled statically.
@@ -248,6 +270,13 @@ hipError_t launch_gemm_down_i8_2(const void* A, const float* sa, const void* B, 
                                  int y_dtype, void* Y, const MTile* sb, const int32_t* cb, int mb, const MTile* ss,
                                  const int32_t* cs, int ms, uint32_t* flags, hipStream_t st, int ksplit = 1,
                                  long long part_elems = 0);
+// the products of few rows (32-row tiles): gate/up with SwiGLU to fp16 h where
+// B1 is given, else y in y_dtype; sched null: rows of one expert, the first
+// *rows_dev (nullable) of static_rows
+hipError_t launch_stream_i8(const void* A, const int32_t* a_rows, const float* sa, const void* B0, const float* sb0,
+                            const void* B1, const float* sb1, int N, int K, int y_dtype, void* out,
+                            const MTile* sched, const int32_t* count, int max_tiles, const int32_t* rows_dev,
+                            int static_rows, uint32_t* flags, hipStream_t st);
 // rows of src (bf16, fp32 or fp16) to int8 codes and a scale per row; rows at
 // and beyond *rows_dev (nullable) are left alone
 hipError_t launch_quant_int8(int src_dtype, const void* src, int rows, int cols, const int32_t* rows_dev, void* codes,
@@ -270,9 +299,13 @@ hipError_t launch_combine_norm(const moe_shape& s, const moe_block& b, int y_dty
                                long long part_stride = 0);
 
 // ---- routing with a balance bias (route_biased.hip) --------------------------------
+// own_flags: the launch writes the flag word itself (else it adds to it);
+// for at most kRouteOwnFlagsTokens tokens, or without k_per_token
+constexpr int kRouteOwnFlagsTokens = 32768;
 hipError_t launch_route_biased(const moe_shape& s, const float* logits, const float* select_bias,
                                const int32_t* k_per_token, int32_t* ids, float* gates, uint32_t* flags,
-                               hipStream_t st, int parts = 1, long long part_stride = 0, float* sum_out = nullptr);
+                               bool own_flags, hipStream_t st, int parts = 1, long long part_stride = 0,
+                               float* sum_out = nullptr);
 
 // ---- expert-parallel exchange over G virtual ranks (ep.hip) -----------------
 constexpr int kMaxRanks = 64;
