@@ -134,6 +134,57 @@ def test_gates_of_scores_that_vanish():
     assert (gates == 0).all()
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,keep,topn", [(256, 1, 1, 1), (256, 8, 4, 2), (72, 6, 2, 3), (16, 1, 1, 1), (512, 4, 3, 1)])
+def test_keys_closer_than_fp32_can_tell(score, E, G, keep, topn):
+    """Logits one fp32 step apart around a few values, and biases that put different logits at nearly one key: the
+    order is that of the fp64 keys."""
+    r = np.random.default_rng(E + G)
+    T = 130
+    base = r.choice(np.array([-2.0, 0.25, 1.0, 1.5], np.float32), size=(T, E))
+    logits = base.copy()
+    for _ in range(3):
+        logits = np.where(r.random((T, E)) < 0.5, np.nextafter(logits, np.float32(9)), logits)
+    check(logits, np.zeros(E), 8, score=score, G=G, keep=keep, topn=topn)
+    if score == "sigmoid":   # sigmoid(1) - sigmoid(0.25) between the two halves, to fp32
+        gap = np.float32(1 / (1 + np.exp(-1.0)) - 1 / (1 + np.exp(-0.25)))
+        logits[:, :E // 2] = np.where(r.random((T, E // 2)) < 0.5, 1.0, np.nextafter(np.float32(1), np.float32(2)))
+        logits[:, E // 2:] = np.where(r.random((T, E // 2)) < 0.5, 0.25, np.nextafter(np.float32(0.25), np.float32(1)))
+        bias = np.zeros(E, np.float32)
+        bias[E // 2:] = gap
+        bias[::3] = np.nextafter(bias[::3], np.float32(1))
+        check(logits, bias, 8, score=score, G=G, keep=keep, topn=topn)
+        check(logits, bias * np.float32(-1e4), 8, score=score, G=G, keep=keep, topn=topn)
+    # one token in which only one pair is close, at every place of the order
+    for j in range(8):
+        one = np.arange(E, 0, -1).astype(np.float32)[None] * np.float32(0.01)
+        one[0, j + 1] = np.nextafter(one[0, j], np.float32(9 if j % 2 else -9))
+        check(one, np.zeros(E), 8, score=score, G=G, keep=keep, topn=topn)
+
+
+@pytest.mark.parametrize("k", [15, 16])
+def test_close_keys_with_every_slot_used(k):
+    r = np.random.default_rng(k)
+    logits = (np.float32(1) + r.integers(0, 40, (50, 128)) * np.float32(2 ** -23)).astype(np.float32)
+    check(logits, np.zeros(128), k)
+    kpt = r.integers(1, k + 1, 50)
+    check(logits, np.zeros(128), k, kpt)
+
+
+def test_many_tokens_with_k_per_token():
+    """More tokens than one launch looks through for bad budgets."""
+    T = 40000
+    lg = W.make_logits(T, 16, "cpu", seed=4).numpy()
+    kpt = np.full(T, 2, np.int32)
+    for bad in (None, T - 1):
+        if bad is not None:
+            kpt[bad] = 5
+        ids, gates, flags = route(lg, np.zeros(16, np.float32), 4, kpt)
+        assert flags == (0 if bad is None else abi.MOE_FLAG_BAD_K)
+        want, _ = P.route_biased(lg[-50:], np.zeros(16), 4, kpt[-50:])
+        assert np.array_equal(ids[-50:], want)
+
+
 def test_k_per_token_and_bad_k():
     r = np.random.default_rng(3)
     logits, bias = r.normal(size=(300, 128)), r.normal(size=128) * 0.1
