@@ -29,16 +29,18 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
 constexpr int granule(int dt) { return dt == MOE_F32 ? 4 : 8; }
 
 template <int DT>
-__device__ __forceinline__ void load_granule(const void* p, size_t i, float* f) {
-  if constexpr (DT == MOE_F32) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+__device__ __forceinline__ u32x4 load_raw(const void* p, size_t i) {
+  return *reinterpret_cast<const u32x4*>(static_cast<const char*>(p) + i * (DT == MOE_F32 ? 4 : 2));
+}
+
+template <int DT>
+__device__ __forceinline__ void widen(const u32x4 w, float* f) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) f[q] = v[q];
-  } else {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t x = w[q];
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t x = w[q];
+    if constexpr (DT == MOE_F32) {
+      f[q] = __uint_as_float(x);
+    } else {
       if constexpr (DT == MOE_BF16) {
         f[2 * q] = __uint_as_float(x << 16);
         f[2 * q + 1] = __uint_as_float(x & 0xFFFF0000u);
@@ -49,6 +51,11 @@ __device__ __forceinline__ void load_granule(const void* p, size_t i, float* f) 
       }
     }
   }
+}
+
+template <int DT>
+__device__ __forceinline__ void load_granule(const void* p, size_t i, float* f) {
+  widen<DT>(load_raw<DT>(p, i), f);
 }
 
 // N consecutive fp32 or bf16 values at element i (i a multiple of N, N 4 or 8)
@@ -239,48 +246,56 @@ __global__ __launch_bounds__(NT) void k_combine_norm(const void* __restrict__ y,
                                                      const BlockEnd e) {
   constexpr int G = granule(DT);
   const int t = blockIdx.x;
-  __shared__ int s_row[KM];
-  __shared__ float s_g[KM];
-  if (threadIdx.x < KM) {
-    const bool live = (int)threadIdx.x < k_max;
-    s_row[threadIdx.x] = live ? row_of_slot[(size_t)t * k_max + threadIdx.x] : -1;
-    s_g[threadIdx.x] = live ? gates[(size_t)t * k_max + threadIdx.x] : 0.f;
+  // the token's slots, uniform over the block (scalar registers).  A slot
+  // without a row loads the row of a slot that has one (from the cache) and
+  // masks it to zeros, so that no load waits behind a branch
+  int row[KM], any = 0;
+  uint32_t live[KM];
+  float weight[KM];
+#pragma unroll
+  for (int j = 0; j < KM; ++j) {
+    const int r = j < k_max ? row_of_slot[(size_t)t * k_max + j] : -1;
+    live[j] = r >= 0 ? 0xFFFFFFFFu : 0u;
+    weight[j] = r >= 0 ? gates[(size_t)t * k_max + j] : 0.f;
+    row[j] = r;
+    if (r >= 0) any = r;
   }
-  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < KM; ++j) row[j] = live[j] ? row[j] : any;
   const int granules = H / G;
   float acc[V > 0 ? V : 1][G];
   float sum = 0.f;
+  const void* last = shared ? shared : y;
+  const size_t last_row = shared ? (size_t)t : (size_t)any;
+  const uint32_t last_live = shared ? 0xFFFFFFFFu : 0u;
   auto take = [&](int g, float* a) {
-    float v[KM][G];
+    u32x4 raw[KM + 1];
 #pragma unroll
-    for (int j = 0; j < KM; ++j) {
-      const int r = s_row[j];
-      if (r < 0) continue;
-      load_granule<DT>(y, (size_t)r * H + (size_t)g * G, v[j]);
-      if constexpr (DT == MOE_F32) {
-        for (int p = 1; p < parts; ++p) {
-          float w[G];
-          load_granule<DT>(static_cast<const float*>(y) + p * part_stride, (size_t)r * H + (size_t)g * G, w);
-#pragma unroll
-          for (int q = 0; q < G; ++q) v[j][q] += w[q];
-        }
-      }
-    }
+    for (int j = 0; j < KM; ++j) raw[j] = load_raw<DT>(y, (size_t)row[j] * H + (size_t)g * G);
+    raw[KM] = load_raw<DT>(last, last_row * H + (size_t)g * G);
 #pragma unroll
     for (int q = 0; q < G; ++q) a[q] = 0.f;
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
-      if (s_row[j] < 0) continue;
-      const float w = s_g[j];
+      float v[G];
+      widen<DT>(raw[j] & live[j], v);
+      if constexpr (DT == MOE_F32) {
+        if (live[j]) {
+          for (int p = 1; p < parts; ++p) {
+            float w[G];
+            load_granule<DT>(static_cast<const float*>(y) + p * part_stride, (size_t)row[j] * H + (size_t)g * G, w);
 #pragma unroll
-      for (int q = 0; q < G; ++q) a[q] = fmaf(w, v[j][q], a[q]);
-    }
-    if (shared) {
-      float w[G];
-      load_granule<DT>(shared, (size_t)t * H + (size_t)g * G, w);
+            for (int q = 0; q < G; ++q) v[q] += w[q];
+          }
+        }
+      }
 #pragma unroll
-      for (int q = 0; q < G; ++q) a[q] += w[q];
+      for (int q = 0; q < G; ++q) a[q] = fmaf(weight[j], v[q], a[q]);
     }
+    float v[G];
+    widen<DT>(raw[KM] & last_live, v);
+#pragma unroll
+    for (int q = 0; q < G; ++q) a[q] += v[q];
 #pragma unroll
     for (int q = 0; q < G; ++q) sum = fmaf(a[q], a[q], sum);
   };
