@@ -127,7 +127,8 @@ __device__ __forceinline__ void block_sum_max(float& sum, float& top) {
 template <int DT, int V, int NT, bool NORM>
 __global__ __launch_bounds__(NT) void k_rows(int cols, const void* x, const float* __restrict__ weight, float eps,
                                              int out_bf16, void* out, uint8_t* __restrict__ codes,
-                                             float* __restrict__ scales, const int32_t* __restrict__ rows_dev) {
+                                             float* __restrict__ scales, const int32_t* __restrict__ rows_dev,
+                                             uint32_t* __restrict__ h_flags) {
   constexpr int G = granule(DT);
   const int r = blockIdx.x;
   if (rows_dev && r >= *rows_dev) return;  // uniform over the block
@@ -135,8 +136,18 @@ __global__ __launch_bounds__(NT) void k_rows(int cols, const void* x, const floa
   const size_t base = (size_t)r * cols;
   float t[V > 0 ? V : 1][G];
   float sum = 0.f, top = 0.f;
+  bool range = false;
   auto take = [&](int g, float* f) {  // t of granule g, its squares and maximum
     load_granule<DT>(x, base + (size_t)g * G, f);
+    if constexpr (DT == MOE_F16) {
+      if (h_flags) {
+#pragma unroll
+        for (int q = 0; q < G; ++q) {
+          if (fabsf(f[q]) > 65504.f) range = true;
+          f[q] = fminf(fmaxf(f[q], -65504.f), 65504.f);
+        }
+      }
+    }
     if constexpr (NORM) {
       float w[G];
       if (weight) load_stream<G>(weight, false, (size_t)g * G, w);
@@ -193,17 +204,18 @@ __global__ __launch_bounds__(NT) void k_rows(int cols, const void* x, const floa
       put(g, t[0]);
     }
   }
+  if (DT == MOE_F16 && range) atomicOr(h_flags, (uint32_t)MOE_FLAG_H_RANGE);
   if (scales && threadIdx.x == 0) scales[r] = NORM ? top * rstd / 127.0f : top / 127.0f;
 }
 
 template <int DT, bool NORM>
 hipError_t launch_rows(int rows, int cols, const void* x, const float* weight, float eps, int out_dtype, void* out,
-                       void* codes, float* scales, const int32_t* rows_dev, hipStream_t st) {
+                       void* codes, float* scales, const int32_t* rows_dev, uint32_t* h_flags, hipStream_t st) {
   if (rows <= 0) return hipSuccess;
   const int granules = cols / granule(DT);
 #define MOE_ROWS(V, NT)                                                                                      \
   hipLaunchKernelGGL((k_rows<DT, V, NT, NORM>), dim3(rows), dim3(NT), 0, st, cols, x, weight, eps,           \
-                     out_dtype == MOE_BF16 ? 1 : 0, out, static_cast<uint8_t*>(codes), scales, rows_dev)
+                     out_dtype == MOE_BF16 ? 1 : 0, out, static_cast<uint8_t*>(codes), scales, rows_dev, h_flags)
   if (granules <= 64) MOE_ROWS(1, 64);
   else if (granules <= 256) MOE_ROWS(1, 256);
   else if (granules <= 512) MOE_ROWS(2, 256);
@@ -387,17 +399,19 @@ hipError_t launch_end_k(const moe_shape& s, const void* y, const int32_t* row_of
 hipError_t launch_norm(int rows, int cols, int src_dtype, const void* x, const float* weight, float eps,
                        int out_dtype, void* out, void* codes, float* scales, hipStream_t st) {
   if (src_dtype == MOE_BF16)
-    return launch_rows<MOE_BF16, true>(rows, cols, x, weight, eps, out_dtype, out, codes, scales, nullptr, st);
-  return launch_rows<MOE_F32, true>(rows, cols, x, weight, eps, out_dtype, out, codes, scales, nullptr, st);
+    return launch_rows<MOE_BF16, true>(rows, cols, x, weight, eps, out_dtype, out, codes, scales, nullptr, nullptr, st);
+  return launch_rows<MOE_F32, true>(rows, cols, x, weight, eps, out_dtype, out, codes, scales, nullptr, nullptr, st);
 }
 
 hipError_t launch_quant_int8(int src_dtype, const void* src, int rows, int cols, const int32_t* rows_dev, void* codes,
-                             float* scales, hipStream_t st) {
+                             float* scales, hipStream_t st, uint32_t* h_flags) {
   if (src_dtype == MOE_BF16)
-    return launch_rows<MOE_BF16, false>(rows, cols, src, nullptr, 0.f, 0, nullptr, codes, scales, rows_dev, st);
+    return launch_rows<MOE_BF16, false>(rows, cols, src, nullptr, 0.f, 0, nullptr, codes, scales, rows_dev, nullptr,
+                                        st);
   if (src_dtype == MOE_F16)
-    return launch_rows<MOE_F16, false>(rows, cols, src, nullptr, 0.f, 0, nullptr, codes, scales, rows_dev, st);
-  return launch_rows<MOE_F32, false>(rows, cols, src, nullptr, 0.f, 0, nullptr, codes, scales, rows_dev, st);
+    return launch_rows<MOE_F16, false>(rows, cols, src, nullptr, 0.f, 0, nullptr, codes, scales, rows_dev, h_flags,
+                                       st);
+  return launch_rows<MOE_F32, false>(rows, cols, src, nullptr, 0.f, 0, nullptr, codes, scales, rows_dev, nullptr, st);
 }
 
 hipError_t launch_combine_norm(const moe_shape& s, const moe_block& b, int y_dtype, const void* y,

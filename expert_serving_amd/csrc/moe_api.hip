@@ -333,6 +333,11 @@ bool stream_i8(const GemmPlan& gp, const moe_shape& s, long long matrix_bytes) {
   return !gp.has_big() && std::min<long long>(slots, s.num_experts) * matrix_bytes <= kStreamMaxBytes;
 }
 
+// The second product of a batch of few and short rows quantises them itself:
+// every block passes over its tile's rows (at most 16) where a launch would
+// pass over them once.
+bool stream_quantises(int max_rows, int cols) { return max_rows <= 16 && (long long)max_rows * cols <= 16384; }
+
 // Row tiles of a plan without big tiles: each expert that has rows ends with
 // one tile that may be short.
 int stream_tiles(const moe_shape& s, int max_small) {
@@ -621,10 +626,12 @@ moe_status run_shared(const moe_shape& s, const void* x, const void* wsg, const 
 }
 
 // int8 S7-S8: xq rows (gathered through a_rows when given, their scales too).
-// With y_dtype fp32 and ksplit > 1, y holds ksplit partial sums.
+// With y_dtype fp32 and ksplit > 1, y holds ksplit partial sums.  max_rows: the
+// most rows an expert can have.
 moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows, const float* xsc,
                       const int32_t* offsets, const moe_int8_ffn& w, int y_dtype, void* y, void* ws,
-                      const WsLayout& L, hipStream_t st, const moe_debug* dbg, int ksplit, bool clear_flags) {
+                      const WsLayout& L, hipStream_t st, const moe_debug* dbg, int ksplit, bool clear_flags,
+                      int max_rows) {
   const GemmPlan gp = choose_gemm_plan(s);
   const int E = s.num_experts, H = s.hidden, I = s.intermediate;
   const int slots = s.num_tokens * s.top_k;
@@ -636,14 +643,24 @@ moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows,
   void* hq = at<void>(ws, L.hq);
   float* hsc = at<float>(ws, L.hsc);
   const bool merged = gp.has_big() && gp.has_small();
-  const int tiles = stream_tiles(s, L.max_tiles_small);
+  if (L.stream) {
+    const int tiles = stream_tiles(s, L.max_tiles_small);
+    MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, true, st));
+    MOE_HIP(launch_stream_gateup_i8(xq, a_rows, xsc, w, I, H, h, offsets, E, tiles, max_rows, 0, flags, clear_flags,
+                                    st));
+    const bool fused = stream_quantises(max_rows, I);
+    if (!fused) MOE_HIP(launch_quant_int8(MOE_F16, h, slots, I, offsets + E, hq, hsc, st, flags));
+    MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, false, st));
+    MOE_HIP(stage_mark(dbg, MOE_STAGE_DOWN, true, st));
+    MOE_HIP(launch_stream_i8(fused ? h : hq, fused ? nullptr : hsc, w.down, w.down_scales, H, I, y_dtype, y, offsets, E,
+                             tiles, max_rows, 0, flags, false, st));
+    MOE_HIP(stage_mark(dbg, MOE_STAGE_DOWN, false, st));
+    return MOE_OK;
+  }
   MOE_HIP(launch_build_schedule(offsets, E, gp, sb, L.max_tiles_big, ss, L.max_tiles_small, cnt, st,
                                 clear_flags ? flags : nullptr));
   MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, true, st));
-  if (L.stream) {
-    MOE_HIP(launch_stream_i8(xq, a_rows, xsc, w.gate, w.gate_scales, w.up, w.up_scales, I, H, 0, h, ss, cnt + 1, tiles,
-                             nullptr, 0, flags, st));
-  } else if (merged) {
+  if (merged) {
     MOE_HIP(launch_gemm_gateup_i8_2(xq, a_rows, xsc, w.gate, w.gate_scales, w.up, w.up_scales, I, H, h, sb, cnt,
                                     L.max_tiles_big, ss, cnt + 1, L.max_tiles_small, flags, st));
   } else if (L.ks_gu > 1) {
@@ -661,10 +678,7 @@ moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows,
   MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, false, st));
   MOE_HIP(stage_mark(dbg, MOE_STAGE_DOWN, true, st));
   const long long pe = (long long)slots * H;
-  if (L.stream)
-    MOE_HIP(launch_stream_i8(hq, nullptr, hsc, w.down, w.down_scales, nullptr, nullptr, H, I, y_dtype, y, ss, cnt + 1,
-                             tiles, nullptr, 0, flags, st));
-  else if (merged)
+  if (merged)
     MOE_HIP(launch_gemm_down_i8_2(hq, hsc, w.down, w.down_scales, H, I, y_dtype, y, sb, cnt, L.max_tiles_big, ss,
                                   cnt + 1, L.max_tiles_small, flags, st, ksplit, pe));
   else
@@ -683,11 +697,12 @@ moe_status run_shared_i8(const moe_shape& s, const void* xq, const float* xsc, c
   float* hssc = at<float>(ws, L.hssc);
   uint32_t* flags = at<uint32_t>(ws, L.flags);
   if (L.stream_shared) {
-    MOE_HIP(launch_stream_i8(xq, nullptr, xsc, w.gate, w.gate_scales, w.up, w.up_scales, Is, H, 0, hs, nullptr, nullptr,
-                             0, nullptr, T, flags, st));
-    MOE_HIP(launch_quant_int8(MOE_F16, hs, T, Is, nullptr, at<void>(ws, L.hq), hssc, st));
-    MOE_HIP(launch_stream_i8(at<void>(ws, L.hq), nullptr, hssc, w.down, w.down_scales, nullptr, nullptr, H, Is,
-                             y_dtype, at<void>(ws, L.ys), nullptr, nullptr, 0, nullptr, T, flags, st));
+    void* hsq = at<void>(ws, L.hq);
+    MOE_HIP(launch_stream_gateup_i8(xq, nullptr, xsc, w, Is, H, hs, nullptr, 1, 0, T, T, flags, false, st));
+    const bool fused = stream_quantises(T, Is);
+    if (!fused) MOE_HIP(launch_quant_int8(MOE_F16, hs, T, Is, nullptr, hsq, hssc, st, flags));
+    MOE_HIP(launch_stream_i8(fused ? hs : hsq, fused ? nullptr : hssc, w.down, w.down_scales, H, Is, y_dtype,
+                             at<void>(ws, L.ys), nullptr, 1, 0, T, T, flags, false, st));
     return MOE_OK;
   }
   if (L.ks_gus > 1 && bm == 32) {
@@ -920,7 +935,8 @@ moe_status run_block(const moe_shape& s, const moe_block& b, const void* x, cons
   if (experts && !b.pre_norm) MOE_HIP(launch_quant_int8(MOE_BF16, x, T, H, nullptr, xq, xsc, st));
   MOE_HIP(stage_mark(dbg, MOE_STAGE_GATHER, false, st));
   if (experts)
-    MOE_TRY(run_ffn_i8(s, xq, row_token, xsc, offsets, *experts, y_dtype, y, ws, L, st, dbg, L.ksplit, false));
+    MOE_TRY(run_ffn_i8(s, xq, row_token, xsc, offsets, *experts, y_dtype, y, ws, L, st, dbg, L.ksplit, false,
+                       T));  // (a token takes an expert once)
   else
     MOE_TRY(run_ffn(s, xl, row_token, offsets, wt[0], wt[1], wt[2], y, ws, L, st, dbg, L.ksplit, y_half));
   const void* ys = nullptr;
@@ -1431,10 +1447,11 @@ moe_status moe_grouped_gemm_int8(int32_t rows, int32_t n, int32_t k, int32_t num
   const bool split = p.ksplit > 1;
   void* dst = split ? at<void>(ws, p.parts) : y;
   const int dt = split ? MOE_F32 : y_dtype;
-  if (p.stream && num_experts == 1) {
-    MOE_HIP(launch_clear_flags(flags, st));
-    MOE_HIP(launch_stream_i8(a, nullptr, a_scales, b, b_scales, nullptr, nullptr, n, k, y_dtype, y, nullptr, nullptr, 0,
-                             expert_offsets ? expert_offsets + 1 : nullptr, rows, flags, st));
+  if (p.stream) {
+    // (an fp16 y adds to the flag word, which then has to be clear before)
+    if (y_dtype == MOE_F16) MOE_HIP(launch_clear_flags(flags, st));
+    MOE_HIP(launch_stream_i8(a, a_scales, b, b_scales, n, k, y_dtype, y, expert_offsets, num_experts,
+                             stream_tiles(p.s, p.max_small), rows, rows, flags, y_dtype != MOE_F16, st));
     return MOE_OK;
   }
   if (!expert_offsets) {
@@ -1444,10 +1461,7 @@ moe_status moe_grouped_gemm_int8(int32_t rows, int32_t n, int32_t k, int32_t num
                                 p.ksplit, pe));
   } else {
     MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sb, p.max_big, ss, p.max_small, cnt, st, flags));
-    if (p.stream)
-      MOE_HIP(launch_stream_i8(a, nullptr, a_scales, b, b_scales, nullptr, nullptr, n, k, y_dtype, y, ss, cnt + 1,
-                               stream_tiles(p.s, p.max_small), nullptr, 0, flags, st));
-    else if (p.gp.has_big() && p.gp.has_small())
+    if (p.gp.has_big() && p.gp.has_small())
       MOE_HIP(launch_gemm_down_i8_2(a, a_scales, b, b_scales, n, k, dt, dst, sb, cnt, p.max_big, ss, cnt + 1,
                                     p.max_small, flags, st, p.ksplit, pe));
     else
@@ -1487,7 +1501,7 @@ moe_status moe_grouped_ffn_int8(const moe_shape* shape, const int8_t* x_codes, c
   const bool split = L.ksplit > 1;
   void* dst = split ? at<void>(ws, L.y) : y_perm;
   MOE_TRY(run_ffn_i8(s, x_codes, nullptr, x_scales, expert_offsets, *experts, split ? MOE_F32 : y_dtype, dst, ws, L,
-                     st, nullptr, L.ksplit, true));
+                     st, nullptr, L.ksplit, true, s.num_tokens * s.top_k));
   const int slots = s.num_tokens * s.top_k;
   if (split)
     MOE_HIP(launch_sum_parts(at<float>(ws, L.y), L.ksplit, (long long)slots * s.hidden, s.hidden,

@@ -270,17 +270,24 @@ hipError_t launch_gemm_down_i8_2(const void* A, const float* sa, const void* B, 
                                  int y_dtype, void* Y, const MTile* sb, const int32_t* cb, int mb, const MTile* ss,
                                  const int32_t* cs, int ms, uint32_t* flags, hipStream_t st, int ksplit = 1,
                                  long long part_elems = 0);
-// the products of few rows (32-row tiles): gate/up with SwiGLU to fp16 h where
-// B1 is given, else y in y_dtype; sched null: rows of one expert, the first
-// *rows_dev (nullable) of static_rows
-hipError_t launch_stream_i8(const void* A, const int32_t* a_rows, const float* sa, const void* B0, const float* sb0,
-                            const void* B1, const float* sb1, int N, int K, int y_dtype, void* out,
-                            const MTile* sched, const int32_t* count, int max_tiles, const int32_t* rows_dev,
-                            int static_rows, uint32_t* flags, hipStream_t st);
+// The products of few rows (stream_i8.hip).  offsets [E + 1] (null: rows [0,
+// static_rows) of one expert); max_tiles bounds the 32-row tiles, max_rows the
+// rows of an expert.  clear_flags: the launch first clears the flag word (it
+// adds to it only for an fp16 y, so then another launch has to clear it).
+// Gate/up with SwiGLU to fp16 h; values out of fp16's range become infinite.
+hipError_t launch_stream_gateup_i8(const void* A, const int32_t* a_rows, const float* sa, const moe_int8_ffn& w,
+                                   int N, int K, void* h, const int32_t* offsets, int E, int max_tiles,
+                                   int max_rows, int static_rows, uint32_t* flags, bool clear_flags, hipStream_t st);
+// y = sa sb A.B^T in y_dtype.  sa null (max_rows <= 16): A holds fp16 rows,
+// quantised on the way (infinite values: as launch_quant_int8).
+hipError_t launch_stream_i8(const void* A, const float* sa, const void* B, const float* sb, int N, int K, int y_dtype,
+                            void* y, const int32_t* offsets, int E, int max_tiles, int max_rows, int static_rows,
+                            uint32_t* flags, bool clear_flags, hipStream_t st);
 // rows of src (bf16, fp32 or fp16) to int8 codes and a scale per row; rows at
-// and beyond *rows_dev (nullable) are left alone
+// and beyond *rows_dev (nullable) are left alone.  h_flags (nullable, fp16): an
+// infinite value counts as the largest finite one and sets MOE_FLAG_H_RANGE.
 hipError_t launch_quant_int8(int src_dtype, const void* src, int rows, int cols, const int32_t* rows_dev, void* codes,
-                             float* scales, hipStream_t st);
+                             float* scales, hipStream_t st, uint32_t* h_flags = nullptr);
 // h = fp16(silu(g) u) from int32 partial sums (see launch_gemm_gateup_i8_parts)
 hipError_t launch_swiglu_parts_i8(const int32_t* parts, int nparts, long long part_elems, int N,
                                   const int32_t* a_rows, const float* sa, const float* sbg, const float* sbu,
