@@ -324,26 +324,29 @@ int gate_up_parts(long long blocks, int stages, bool rounds) {
   return best;
 }
 
-// int8 products of small row tiles stream their weights (launch_stream_i8)
-// while `weight_bytes`, what the batch's experts hold at most, stays below this;
-// above it the LDS tiles come nearer to the memory's rate.
-constexpr long long kStreamMaxBytes = 160LL << 20;
-bool stream_i8(const GemmPlan& gp, const moe_shape& s, long long matrix_bytes) {
-  const long long slots = (long long)s.num_tokens * s.top_k;
-  return !gp.has_big() && std::min<long long>(slots, s.num_experts) * matrix_bytes <= kStreamMaxBytes;
-}
-
-// The second product of a batch of few and short rows quantises them itself:
-// every block passes over its tile's rows (at most 16) where a launch would
-// pass over them once.
-bool stream_quantises(int max_rows, int cols) { return max_rows <= 16 && (long long)max_rows * cols <= 16384; }
-
 // Row tiles of a plan without big tiles: each expert that has rows ends with
 // one tile that may be short.
 int stream_tiles(const moe_shape& s, int max_small) {
   const long long slots = (long long)s.num_tokens * s.top_k;
   return (int)std::min<long long>(max_small, std::min<long long>(slots, s.num_experts) + slots / 32);
 }
+
+// int8 products of small row tiles stream their weights (launch_stream_i8)
+// while the tiles together read at most this; above it the LDS tiles come nearer
+// to the memory's rate.  Measured, streams against LDS tiles: FFN of 1 token
+// over 128 experts (36 MB) 14.9 against 32.0 us, of 4 tokens (144 MB) 42 against
+// 50, of 16 (576 MB) 104 against 78, of 1 token over 256 larger experts (336 MB)
+// 87 against 77; products of 8 rows of 224 MB 50 against 53 us, of 60 rows (two
+// tiles, 448 MB) 104 against 71.
+constexpr long long kStreamMaxBytes = 240LL << 20;
+bool stream_i8(const GemmPlan& gp, const moe_shape& s, int max_small, long long matrix_bytes) {
+  return !gp.has_big() && stream_tiles(s, max_small) * matrix_bytes <= kStreamMaxBytes;
+}
+
+// The second product of a batch of few and short rows quantises them itself:
+// every block passes over its tile's rows (at most 16) where a launch would
+// pass over them once.
+bool stream_quantises(int max_rows, int cols) { return max_rows <= 16 && (long long)max_rows * cols <= 16384; }
 
 }  // namespace
 
@@ -371,9 +374,9 @@ WsLayout plan_workspace(const moe_shape& s, int format, bool normed) {
       w.ks_gus = gate_up_parts((long long)((T + 31) / 32) * (long long)((Is + 255) / 256), stages, false);
   }
   if (i8) {
-    w.stream = stream_i8(gp, s, 3LL * (long long)(H * I));
+    w.stream = stream_i8(gp, s, w.max_tiles_small, 3LL * (long long)(H * I));
     // the shared expert: a batch whose every row takes one expert
-    w.stream_shared = Is > 0 && T < 64 && 3LL * (long long)(H * Is) <= kStreamMaxBytes;
+    w.stream_shared = Is > 0 && T < 64 && (long long)((T + 31) / 32 * 3 * H * Is) <= kStreamMaxBytes;
     if (w.stream) w.ksplit = w.ks_gu = 1;
     if (w.stream_shared) w.ks_gus = 1;
   }
@@ -743,7 +746,7 @@ GemmI8Plan plan_gemm_i8(int rows, int n, int k, int E) {
   p.s.act_dtype = MOE_BF16;
   p.gp = choose_gemm_plan(p.s);
   tile_bounds(p.s, p.gp, p.max_big, p.max_small);
-  p.stream = stream_i8(p.gp, p.s, (long long)n * k);
+  p.stream = stream_i8(p.gp, p.s, p.max_small, (long long)n * k);
   p.ksplit = p.stream ? 1 : down_parts(p.s, p.gp, p.max_small, true);
   size_t o = 0;
   auto take = [&](size_t bytes) {
