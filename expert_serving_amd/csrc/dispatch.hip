@@ -337,7 +337,7 @@ __global__ __launch_bounds__(512) void k_build_sched(const int32_t* __restrict__
                                                      MTile* __restrict__ sched_big, int max_big,
                                                      MTile* __restrict__ sched_small, int max_small,
                                                      int32_t* __restrict__ count,
-                                                     uint32_t* __restrict__ flags) {
+                                                     uint32_t* __restrict__ flags, int fill_cols) {
   __shared__ int s_big[512], s_small[512];
   const int tid = threadIdx.x;
   if (flags && tid == 0) *flags = 0u;
@@ -379,14 +379,40 @@ __global__ __launch_bounds__(512) void k_build_sched(const int32_t* __restrict__
     s_small[tid] += as;
     __syncthreads();
   }
+  // fill_cols > 0: the column tiles of a launch whose blocks fill every compute
+  // unit, of a kernel that takes tiles of any height.  When a few rounds of
+  // blocks would end with one that keeps at most a quarter of the units busy,
+  // that round's row tiles are cut into kFillSplit parts.
+  const int total = s_big[511];
+  int whole = total;
+  if (fill_cols > 0) {
+    const long long blocks = (long long)total * fill_cols;
+    const int rest = (int)(blocks % kUnits), turn = (rest + fill_cols - 1) / fill_cols;
+    if (rest > 0 && blocks > kUnits && blocks < 5 * kUnits && turn * fill_cols * kFillSplit <= kUnits)
+      whole = total - turn;
+  }
+  const int begin = s_big[tid] - nb, uncut = min(max(whole - begin, 0), nb);
   for (int i = 0; i < nb; ++i) {
-    const int slot = s_big[tid] - nb + i;
-    if (slot < max_big) {
+    const int slot = begin + i;
+    if (i >= uncut) {
+      const int part = bm_big / kFillSplit;
+      for (int q = 0; q < kFillSplit; ++q) {
+        const int at = whole + (slot - whole) * kFillSplit + q;
+        if (at >= max_big) break;
+        MTile m;
+        m.expert = tid;
+        m.row0 = r0 + i * bm_big + q * part;
+        m.rows = max(0, min(part, kept - i * bm_big - q * part));  // 0: behind a short tile
+        m.group = tile_group(q, kFillSplit);
+        sched_big[at] = m;
+      }
+    } else if (slot < max_big) {
       MTile m;
       m.expert = tid;
       m.row0 = r0 + i * bm_big;
       m.rows = min(bm_big, kept - i * bm_big);
-      m.pad = 0;
+      const int g = i / kTileGroup * kTileGroup;
+      m.group = tile_group(i - g, min(kTileGroup, uncut - g));
       sched_big[slot] = m;
     }
   }
@@ -397,12 +423,12 @@ __global__ __launch_bounds__(512) void k_build_sched(const int32_t* __restrict__
       m.expert = tid;
       m.row0 = r0 + sbeg + i * bm_small;
       m.rows = min(bm_small, kept - sbeg - i * bm_small);
-      m.pad = 0;
+      m.group = 0;
       sched_small[slot] = m;
     }
   }
   if (tid == 511) {
-    count[0] = min(s_big[511], max_big);
+    count[0] = min(whole + (total - whole) * kFillSplit, max_big);
     count[1] = min(s_small[511], max_small);
   }
 }
@@ -494,10 +520,10 @@ hipError_t launch_gather(const moe_shape& s, const void* x, const int32_t* row_t
 
 hipError_t launch_build_schedule(const int32_t* offsets, int E, const GemmPlan& plan,
                                  MTile* sched_big, int max_big, MTile* sched_small, int max_small,
-                                 int32_t* count, hipStream_t st, uint32_t* flags) {
+                                 int32_t* count, hipStream_t st, uint32_t* flags, int fill_cols) {
   hipLaunchKernelGGL(k_build_sched, dim3(1), dim3(512), 0, st, offsets, E, plan.bm_big,
                      plan.bm_small, plan.split_rows, plan.tail_rows, sched_big, max_big, sched_small,
-                     max_small, count, flags);
+                     max_small, count, flags, fill_cols);
   return hipGetLastError();
 }
 

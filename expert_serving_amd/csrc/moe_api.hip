@@ -180,7 +180,7 @@ T* at(void* ws, size_t off) {
 // remainder rows of a big expert that ride on one small tile
 constexpr int kTailRows = 64;
 // compute units of one MI355X (8 XCDs x 32)
-constexpr int kComputeUnits = 256;
+constexpr int kComputeUnits = kUnits;
 // K-split parts of the down projection for a batch of a token or two
 constexpr int kFewKsplit = 8;
 // most K-split parts of a gate/up projection (16 keeps each part >= 4 stages
@@ -220,6 +220,17 @@ GemmPlan choose_gemm_plan(const moe_shape& s) {
     // tile costs its full height in MFMA time, while the small tiles stream
     // the expert's weights beside the big tiles of the same launch
     p.tail_rows = kTailRows;
+  }
+  return p;
+}
+
+// int8 products: 32-row tiles below 64 rows per expert, else tiles of up to 256
+// rows that run at the height of their rows (no small class).
+GemmPlan choose_gemm_plan_i8(const moe_shape& s) {
+  GemmPlan p = choose_gemm_plan(s);
+  if (p.has_big()) {
+    p.split_rows = 0;
+    p.tail_rows = 0;
   }
   return p;
 }
@@ -357,7 +368,7 @@ WsLayout plan_workspace(const moe_shape& s, int format, bool normed) {
   const size_t H = (size_t)s.hidden, I = (size_t)s.intermediate, Is = (size_t)s.shared_intermediate;
   const size_t eb = mx ? 1 : (size_t)elem_bytes(s.act_dtype);  // bytes of an h element
   const size_t slots = T * k;
-  const GemmPlan gp = choose_gemm_plan(s);
+  const GemmPlan gp = i8 ? choose_gemm_plan_i8(s) : choose_gemm_plan(s);
   w.n_dispatch_tiles = (int)((slots + kDispatchTileSlots - 1) / kDispatchTileSlots);
   tile_bounds(s, gp, w.max_tiles_big, w.max_tiles_small);
   w.ksplit = down_parts(s, gp, w.max_tiles_small, mx || i8);
@@ -374,6 +385,7 @@ WsLayout plan_workspace(const moe_shape& s, int format, bool normed) {
       w.ks_gus = gate_up_parts((long long)((T + 31) / 32) * (long long)((Is + 255) / 256), stages, false);
   }
   if (i8) {
+    if (gp.has_big()) w.max_tiles_big += kUnits;  // (cut tiles)
     w.stream = stream_i8(gp, s, w.max_tiles_small, 3LL * (long long)(H * I));
     // the shared expert: a batch whose every row takes one expert
     w.stream_shared = Is > 0 && T < 64 && (long long)((T + 31) / 32 * 3 * H * Is) <= kStreamMaxBytes;
@@ -635,7 +647,7 @@ moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows,
                       const int32_t* offsets, const moe_int8_ffn& w, int y_dtype, void* y, void* ws,
                       const WsLayout& L, hipStream_t st, const moe_debug* dbg, int ksplit, bool clear_flags,
                       int max_rows) {
-  const GemmPlan gp = choose_gemm_plan(s);
+  const GemmPlan gp = choose_gemm_plan_i8(s);
   const int E = s.num_experts, H = s.hidden, I = s.intermediate;
   const int slots = s.num_tokens * s.top_k;
   MTile* sb = at<MTile>(ws, L.sched_big);
@@ -645,7 +657,6 @@ moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows,
   void* h = at<void>(ws, L.h);
   void* hq = at<void>(ws, L.hq);
   float* hsc = at<float>(ws, L.hsc);
-  const bool merged = gp.has_big() && gp.has_small();
   if (L.stream) {
     const int tiles = stream_tiles(s, L.max_tiles_small);
     MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, true, st));
@@ -660,12 +671,13 @@ moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows,
     MOE_HIP(stage_mark(dbg, MOE_STAGE_DOWN, false, st));
     return MOE_OK;
   }
+  // (the down projection has the fewer column tiles, so the fewer rounds)
   MOE_HIP(launch_build_schedule(offsets, E, gp, sb, L.max_tiles_big, ss, L.max_tiles_small, cnt, st,
-                                clear_flags ? flags : nullptr));
+                                clear_flags ? flags : nullptr, gp.has_big() && ksplit == 1 ? (H + 255) / 256 : 0));
   MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, true, st));
-  if (merged) {
-    MOE_HIP(launch_gemm_gateup_i8_2(xq, a_rows, xsc, w.gate, w.gate_scales, w.up, w.up_scales, I, H, h, sb, cnt,
-                                    L.max_tiles_big, ss, cnt + 1, L.max_tiles_small, flags, st));
+  if (gp.has_big()) {
+    MOE_HIP(launch_gemm_gateup_i8_rows(xq, a_rows, xsc, w.gate, w.gate_scales, w.up, w.up_scales, I, H, h, sb, cnt,
+                                       L.max_tiles_big, flags, st));
   } else if (L.ks_gu > 1) {
     int32_t* parts = at<int32_t>(ws, L.gu_parts);
     const long long pe = (long long)slots * I;
@@ -681,9 +693,9 @@ moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows,
   MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, false, st));
   MOE_HIP(stage_mark(dbg, MOE_STAGE_DOWN, true, st));
   const long long pe = (long long)slots * H;
-  if (merged)
-    MOE_HIP(launch_gemm_down_i8_2(hq, hsc, w.down, w.down_scales, H, I, y_dtype, y, sb, cnt, L.max_tiles_big, ss,
-                                  cnt + 1, L.max_tiles_small, flags, st, ksplit, pe));
+  if (gp.has_big())
+    MOE_HIP(launch_gemm_down_i8_rows(hq, hsc, w.down, w.down_scales, H, I, y_dtype, y, sb, cnt, L.max_tiles_big, flags,
+                                     st, ksplit, pe));
   else
     MOE_HIP(launch_gemm_down_i8(gp.bm_small, hq, hsc, w.down, w.down_scales, H, I, y_dtype, y, ss, cnt + 1,
                                 L.max_tiles_small, 0, flags, st, ksplit, pe));
@@ -744,8 +756,9 @@ GemmI8Plan plan_gemm_i8(int rows, int n, int k, int E) {
   p.s.top_k = 1;
   p.s.num_groups = 1;
   p.s.act_dtype = MOE_BF16;
-  p.gp = choose_gemm_plan(p.s);
+  p.gp = choose_gemm_plan_i8(p.s);
   tile_bounds(p.s, p.gp, p.max_big, p.max_small);
+  if (p.gp.has_big()) p.max_big += kUnits;  // (cut tiles)
   p.stream = stream_i8(p.gp, p.s, p.max_small, (long long)n * k);
   p.ksplit = p.stream ? 1 : down_parts(p.s, p.gp, p.max_small, true);
   size_t o = 0;
@@ -1463,10 +1476,11 @@ moe_status moe_grouped_gemm_int8(int32_t rows, int32_t n, int32_t k, int32_t num
     MOE_HIP(launch_gemm_down_i8(bm, a, a_scales, b, b_scales, n, k, dt, dst, nullptr, nullptr, 0, rows, flags, st,
                                 p.ksplit, pe));
   } else {
-    MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sb, p.max_big, ss, p.max_small, cnt, st, flags));
-    if (p.gp.has_big() && p.gp.has_small())
-      MOE_HIP(launch_gemm_down_i8_2(a, a_scales, b, b_scales, n, k, dt, dst, sb, cnt, p.max_big, ss, cnt + 1,
-                                    p.max_small, flags, st, p.ksplit, pe));
+    MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sb, p.max_big, ss, p.max_small, cnt, st, flags,
+                                  p.gp.has_big() && !split ? (n + 255) / 256 : 0));
+    if (p.gp.has_big())
+      MOE_HIP(launch_gemm_down_i8_rows(a, a_scales, b, b_scales, n, k, dt, dst, sb, cnt, p.max_big, flags, st, p.ksplit,
+                                       pe));
     else
       MOE_HIP(launch_gemm_down_i8(p.gp.bm_small, a, a_scales, b, b_scales, n, k, dt, dst, ss, cnt + 1, p.max_small,
                                   0, flags, st, p.ksplit, pe));

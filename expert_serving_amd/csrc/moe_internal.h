@@ -16,13 +16,20 @@ constexpr int kMaxTopK = 16;
 constexpr int kDispatchTileSlots = 1024;  // slots per dispatch tile (one block)
 
 // One row-tile of the grouped GEMM: `rows` (1..BM) consecutive permuted rows
-// starting at row0, all belonging to `expert`.
+// starting at row0, all belonging to `expert`.  group: for big tiles, the tile's
+// place among up to kTileGroup neighbours of its expert, and their number
+// (tile_group), which a launch may take column by column.
 struct MTile {
   int expert;
   int row0;
   int rows;
-  int pad;
+  int group;
 };
+constexpr int kTileGroup = 8;
+__host__ __device__ constexpr int tile_group(int place, int size) { return (size << 8) | place; }
+
+// compute units of one MI355X (8 XCDs x 32)
+constexpr int kUnits = 256;
 
 // Byte offsets of every region inside the caller's workspace.
 // MXFP8 layers add the quantised x (xq, scales xsc with stride T, and the
@@ -139,10 +146,14 @@ hipError_t launch_gather(const moe_shape& s, const void* x, const int32_t* row_t
                          const int32_t* offsets, void* x_perm, hipStream_t st);
 
 // Both tile lists (see GemmPlan); count[0] = big tiles, count[1] = small tiles.
-// flags (nullable) is cleared.
+// flags (nullable) is cleared.  fill_cols > 0 (kernels that take tiles of any
+// height): the column tiles of the launch; the row tiles of a sparse last
+// round are cut in kFillSplit (some parts without rows; the list needs room
+// for kUnits more).
+constexpr int kFillSplit = 4;
 hipError_t launch_build_schedule(const int32_t* offsets, int E, const GemmPlan& plan,
                                  MTile* sched_big, int max_big, MTile* sched_small, int max_small,
-                                 int32_t* count, hipStream_t st, uint32_t* flags = nullptr);
+                                 int32_t* count, hipStream_t st, uint32_t* flags = nullptr, int fill_cols = 0);
 
 // Grouped GEMMs.  `sched`/`count` give the row tiles; when sched == nullptr
 // the rows [0, static_rows) form one group (expert 0) tiled statically.
@@ -261,15 +272,14 @@ hipError_t launch_gemm_down_i8(int bm, const void* A, const float* sa, const voi
                                int y_dtype, void* Y, const MTile* sched, const int32_t* count, int max_tiles,
                                int static_rows, uint32_t* flags, hipStream_t st, int ksplit = 1,
                                long long part_elems = 0);
-// both row-tile classes in one interleaved launch
-hipError_t launch_gemm_gateup_i8_2(const void* A, const int32_t* a_rows, const float* sa, const void* Bg,
-                                   const float* sbg, const void* Bu, const float* sbu, int N, int K, void* h,
-                                   const MTile* sb, const int32_t* cb, int mb, const MTile* ss, const int32_t* cs,
-                                   int ms, uint32_t* flags, hipStream_t st);
-hipError_t launch_gemm_down_i8_2(const void* A, const float* sa, const void* B, const float* sb_w, int N, int K,
-                                 int y_dtype, void* Y, const MTile* sb, const int32_t* cb, int mb, const MTile* ss,
-                                 const int32_t* cs, int ms, uint32_t* flags, hipStream_t st, int ksplit = 1,
-                                 long long part_elems = 0);
+// row tiles of up to 256 rows, each at the height its rows need
+hipError_t launch_gemm_gateup_i8_rows(const void* A, const int32_t* a_rows, const float* sa, const void* Bg,
+                                      const float* sbg, const void* Bu, const float* sbu, int N, int K, void* h,
+                                      const MTile* sched, const int32_t* count, int max_tiles, uint32_t* flags,
+                                      hipStream_t st);
+hipError_t launch_gemm_down_i8_rows(const void* A, const float* sa, const void* B, const float* sb, int N, int K,
+                                    int y_dtype, void* Y, const MTile* sched, const int32_t* count, int max_tiles,
+                                    uint32_t* flags, hipStream_t st, int ksplit = 1, long long part_elems = 0);
 // The products of few rows (stream_i8.hip).  offsets [E + 1] (null: rows [0,
 // static_rows) of one expert); max_tiles bounds the 32-row tiles, max_rows the
 // rows of an expert.  clear_flags: the launch first clears the flag word (it

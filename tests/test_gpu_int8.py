@@ -97,6 +97,9 @@ GEMM_CASES = [
     ([1, 0, 5, 0], 144, 512, 0), ([64] * 3, 256, 256, 0), ([200, 0, 31, 1], 528, 640, 9), ([130], 1040, 896, 5),
     ([256, 257, 3, 64, 65, 33], 256, 384, 0), ([700], 512, 1024, 0), ([0, 0, 0], 128, 128, 4),
     ([3] * 40 + [0] * 20, 96, 256, 1), ([2100], 160, 256, 0),
+    # column tiles x big row tiles just over a few rounds of the compute units: the last row tiles become small ones,
+    # one of them of a short row tile
+    ([256 * 32, 200], 2048, 128, 3), ([150, 256 * 20 + 130, 256 * 12 + 80], 2048, 128, 0), ([256 * 17], 4096, 128, 0),
 ]
 
 
