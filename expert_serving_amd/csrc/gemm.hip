@@ -839,108 +839,93 @@ __device__ __forceinline__ void gemm_tile(
               (uint8_t)sb;
       }
     }
-  } else if constexpr (MODE == kGateUpI8) {
-    // fp16 h from the int32 sums, stored as below; N is a multiple of 16, so
-    // a group of four columns is all in or out, a 32-column block may be cut
+  } else if constexpr (MODE == kGateUpI8 || MODE == kDownI8) {
+    // h = silu(s sb0 acc0) * (s sb1 acc1) in fp16, or y = s sb0 acc0 in its type.
+    // N is a multiple of 16: a run of eight columns is all in or out.  The
+    // scales are loaded together, one latency for the tile.
     const float* sa = reinterpret_cast<const float*>(mx.sa);
-    const float* sg = reinterpret_cast<const float*>(mx.sb0) + (size_t)expert * N;
-    const float* su = reinterpret_cast<const float*>(mx.sb1) + (size_t)expert * N;
+    const float* sb0 = reinterpret_cast<const float*>(mx.sb0) + (size_t)expert * N;
+    const float* sb1 = reinterpret_cast<const float*>(mx.sb1) + (size_t)expert * N;
+    float s[FM];
+    f32x4 w0[FN][4], w1[DUAL ? FN : 1][4];
 #pragma unroll
     for (int b = 0; b < FM; ++b) {
-      const int m = wm * WM + b * 32 + fr;
-      const int rr = row0 + min(m, rows - 1);
-      const float s = sa[a_rows ? a_rows[rr] : rr];
-#pragma unroll
-      for (int a = 0; a < FN; ++a) {
-        const int nb = n0 + wn * WN + a * 32;
-        uint32_t px[4], py[4];
-        bool ovf = false;
-#pragma unroll
-        for (int qi = 0; qi < 4; ++qi) {
-          const int nc = min(nb + 8 * qi + 4 * fk, N - 4);
-          const f32x4 g4 = *reinterpret_cast<const f32x4*>(sg + nc);
-          const f32x4 u4 = *reinterpret_cast<const f32x4*>(su + nc);
-          float h[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            h[q] = silu_mul_exact((float)acc0[a][b][4 * qi + q] * (s * g4[q]),
-                                  (float)acc1[a][b][4 * qi + q] * (s * u4[q]));
-            ovf |= !(fabsf(h[q]) <= 65504.f) && nb + 8 * qi + 4 * fk < N;
-            h[q] = fminf(fmaxf(h[q], -65504.f), 65504.f);
-          }
-          px[qi] = f32_to_f16_bits(h[0]) | (f32_to_f16_bits(h[1]) << 16);
-          py[qi] = f32_to_f16_bits(h[2]) | (f32_to_f16_bits(h[3]) << 16);
-        }
-        const auto x02 = __builtin_amdgcn_permlane32_swap(px[0], px[2], false, false);
-        const auto y02 = __builtin_amdgcn_permlane32_swap(py[0], py[2], false, false);
-        const auto x13 = __builtin_amdgcn_permlane32_swap(px[1], px[3], false, false);
-        const auto y13 = __builtin_amdgcn_permlane32_swap(py[1], py[3], false, false);
-        if (m >= rows) continue;
-        overflow |= ovf;
-        const int nc = nb + 16 * fk;  // this lane's 16 columns
-        if (nc >= N) continue;
-        uint16_t* dst = static_cast<uint16_t*>(Out) + (size_t)(row0 + m) * ldo + nc;
-        *reinterpret_cast<u32x4*>(dst) = u32x4{x02[0], y02[0], x02[1], y02[1]};
-        *reinterpret_cast<u32x4*>(dst + 8) = u32x4{x13[0], y13[0], x13[1], y13[1]};
-      }
+      const int rr = row0 + min(wm * WM + b * 32 + fr, rows - 1);
+      s[b] = sa[DUAL && a_rows ? a_rows[rr] : rr];
     }
-  } else if constexpr (MODE == kDownI8) {
-    // y = sa sb (int32 sum), fp32 as four-column runs, or 16-bit values
-    // exchanged between lane halves and stored 16 columns per lane
-    const float* sa = reinterpret_cast<const float*>(mx.sa);
-    const float* sb = reinterpret_cast<const float*>(mx.sb0) + (size_t)expert * N;
-    const int ydt = mx.sout_stride;
 #pragma unroll
-    for (int b = 0; b < FM; ++b) {
-      const int m = wm * WM + b * 32 + fr;
-      const float s = sa[row0 + min(m, rows - 1)];
+    for (int a = 0; a < FN; ++a)
 #pragma unroll
-      for (int a = 0; a < FN; ++a) {
-        const int nb = n0 + wn * WN + a * 32;
-        f32x4 v[4];
+      for (int qi = 0; qi < 4; ++qi) {
+        const int nc = min(n0 + wn * WN + a * 32 + 8 * qi + 4 * fk, N - 4);
+        w0[a][qi] = *reinterpret_cast<const f32x4*>(sb0 + nc);
+        if constexpr (DUAL) w1[a][qi] = *reinterpret_cast<const f32x4*>(sb1 + nc);
+      }
+    const int ydt = DUAL ? (int)MOE_F16 : mx.sout_stride;
+    if (ydt == MOE_F32) {
 #pragma unroll
-        for (int qi = 0; qi < 4; ++qi) {
-          const f32x4 b4 = *reinterpret_cast<const f32x4*>(sb + min(nb + 8 * qi + 4 * fk, N - 4));
+      for (int b = 0; b < FM; ++b) {
+        const int m = wm * WM + b * 32 + fr;
+        if (m >= rows) continue;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[qi][q] = (float)acc0[a][b][4 * qi + q] * (s * b4[q]);
-        }
-        if (ydt == MOE_F32) {
-          if (m >= rows) continue;
+        for (int a = 0; a < FN; ++a)
 #pragma unroll
           for (int qi = 0; qi < 4; ++qi) {
-            const int n = nb + 8 * qi + 4 * fk;
-            if (n < N) *reinterpret_cast<f32x4*>(static_cast<float*>(Out) + (size_t)(row0 + m) * ldo + n) = v[qi];
+            const int n = n0 + wn * WN + a * 32 + 8 * qi + 4 * fk;
+            f32x4 v;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = (float)acc0[a][b][4 * qi + q] * (s[b] * w0[a][qi][q]);
+            if (n < N) *reinterpret_cast<f32x4*>(static_cast<float*>(Out) + (size_t)(row0 + m) * ldo + n) = v;
           }
-          continue;
-        }
-        uint32_t px[4], py[4];
-        bool ovf = false;
+      }
+    } else {
+      // 16-bit values go through LDS, free since the main loop's last barrier:
+      // each wavefront lays out its own WM x WN part (16-byte chunks swizzled by
+      // row: the lanes of a store or load phase hit distinct banks) and stores
+      // it as whole runs of a row, 128 bytes (64 for WN = 32) where the
+      // fragments hold 8.
+      constexpr int CH = WN / 8;                 // chunks of a row
+      uint16_t* part = smem + wave * (WM * WN);
+      auto place = [&](int row, int ch) {
+        return row * WN + ((ch ^ (CH == 8 ? row & 7 : (row >> 1) & 3)) << 3);
+      };
+      static_assert(WN == 64 || WN == 32, "chunk swizzle");
 #pragma unroll
-        for (int qi = 0; qi < 4; ++qi) {
-          uint32_t w[4];
+      for (int b = 0; b < FM; ++b) {
+        const bool real = wm * WM + b * 32 + fr < rows;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (ydt == MOE_F16) {
-              ovf |= !(fabsf(v[qi][q]) <= 65504.f) && nb + 8 * qi + 4 * fk < N;
-              w[q] = f32_to_f16_bits(v[qi][q]);
-            } else {
-              w[q] = f32_to_bf16_rne(v[qi][q]);
+        for (int a = 0; a < FN; ++a)
+#pragma unroll
+          for (int qi = 0; qi < 4; ++qi) {
+            const bool in = n0 + wn * WN + a * 32 + 8 * qi < N;
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float v = (float)acc0[a][b][4 * qi + q] * (s[b] * w0[a][qi][q]);
+              if constexpr (DUAL)
+                v = silu_mul_exact(v, (float)acc1[DUAL ? a : 0][DUAL ? b : 0][4 * qi + q] * (s[b] * w1[DUAL ? a : 0][qi][q]));
+              if (ydt == MOE_F16) {
+                overflow |= real && in && !(fabsf(v) <= 65504.f);
+                if constexpr (DUAL) v = fminf(fmaxf(v, -65504.f), 65504.f);
+                w[q] = f32_to_f16_bits(v);
+              } else {
+                w[q] = f32_to_bf16_rne(v);
+              }
             }
+            *reinterpret_cast<u32x2*>(part + place(b * 32 + fr, a * 4 + qi) + 4 * fk) =
+                u32x2{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
           }
-          px[qi] = w[0] | (w[1] << 16);
-          py[qi] = w[2] | (w[3] << 16);
-        }
-        const auto x02 = __builtin_amdgcn_permlane32_swap(px[0], px[2], false, false);
-        const auto y02 = __builtin_amdgcn_permlane32_swap(py[0], py[2], false, false);
-        const auto x13 = __builtin_amdgcn_permlane32_swap(px[1], px[3], false, false);
-        const auto y13 = __builtin_amdgcn_permlane32_swap(py[1], py[3], false, false);
-        if (m >= rows) continue;
-        overflow |= ovf;
-        const int nc = nb + 16 * fk;
-        if (nc >= N) continue;
-        uint16_t* dst = static_cast<uint16_t*>(Out) + (size_t)(row0 + m) * ldo + nc;
-        *reinterpret_cast<u32x4*>(dst) = u32x4{x02[0], y02[0], x02[1], y02[1]};
-        *reinterpret_cast<u32x4*>(dst + 8) = u32x4{x13[0], y13[0], x13[1], y13[1]};
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      constexpr int RPL = 64 / CH;               // rows of a load
+#pragma unroll
+      for (int i = 0; i < WM / RPL; ++i) {
+        const int r = i * RPL + lane / CH, ch = lane % CH;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(part + place(r, ch));
+        const int m = wm * WM + r, n = n0 + wn * WN + 8 * ch;
+        if (m < rows && n < N)
+          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(Out) + (size_t)(row0 + m) * ldo + n) = v;
       }
     }
   } else if constexpr (MODE == kGateUpI8Part) {
