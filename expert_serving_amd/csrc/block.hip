@@ -216,7 +216,14 @@ hipError_t launch_rows(int rows, int cols, const void* x, const float* weight, f
 #define MOE_ROWS(V, NT)                                                                                      \
   hipLaunchKernelGGL((k_rows<DT, V, NT, NORM>), dim3(rows), dim3(NT), 0, st, cols, x, weight, eps,           \
                      out_dtype == MOE_BF16 ? 1 : 0, out, static_cast<uint8_t*>(codes), scales, rows_dev, h_flags)
+  // many short rows to quantise: a wavefront each, without the block's barrier
+  // (65536 rows of 1024 fp16 39 against 58 us, of 2048 85 against 91); fewer or
+  // longer ones, and the norm with its weight: a block each (8192 rows of 2048
+  // fp32: 14 against 16 us)
+  const bool waves = !NORM && rows >= 16384;
   if (granules <= 64) MOE_ROWS(1, 64);
+  else if (waves && granules <= 128) MOE_ROWS(2, 64);
+  else if (waves && granules <= 256) MOE_ROWS(4, 64);
   else if (granules <= 256) MOE_ROWS(1, 256);
   else if (granules <= 512) MOE_ROWS(2, 256);
   else if (granules <= 1024) MOE_ROWS(4, 256);

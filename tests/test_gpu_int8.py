@@ -69,6 +69,19 @@ def test_quantize_zero_tiny_and_huge_rows(dt):
     assert np.all(np.abs(scales.cpu().double().numpy() - s) <= P.U32 * s + 2.0 ** -150)
 
 
+@pytest.mark.parametrize("dt,cols", [("f16", 1024), ("bf16", 1408), ("f32", 896), ("f16", 2048)])
+def test_quantize_many_short_rows(dt, cols):
+    """16384 rows and more of up to 256 16-byte granules take a wavefront each."""
+    g = torch.Generator(device=dev())
+    g.manual_seed(cols)
+    x = (torch.randn(16385, cols, generator=g, device=dev()) * 3).to(DT[dt][0])
+    codes, scales = abi.quantize_int8(x)
+    top = x.double().abs().amax(1, keepdim=True)
+    q = 127 * x.double() / top
+    assert torch.all((codes.double() - q).abs() <= 0.5 + (127 * 2 * P.U32 if dt == "f32" else 0))
+    assert torch.all((scales.double() - top[:, 0] / 127).abs() <= P.U32 * top[:, 0] / 127)
+
+
 def test_quantize_past_32_bit_offsets():
     rows, cols = 270000, 8192                      # 2.2e9 values
     x = torch.empty(rows, cols, device=dev(), dtype=torch.bfloat16)
