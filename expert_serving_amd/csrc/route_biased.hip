@@ -6,15 +6,21 @@
 // one implementation to the next, while two fp64 keys that differ at all
 // differ by far more than fp64 rounding for any logits and biases given in
 // fp32.  fp64 exponentials and compares of every expert would bound the kernel
-// (8192 tokens of 256 experts: 26 us against 9 now), so a token is first routed
+// (8192 tokens of 256 experts: 26 us), so a token is first routed
 // on fp32 keys with a bound on their error; where any decision -- the next expert
 // of a slot, the last group kept -- falls within the bound, which random logits
 // do for a few tokens in ten thousand, the wavefront routes that token again in
 // fp64.  Gates are fp64 either way, of the chosen experts only.
 //
 // fp32 keys: a row of 16 lanes per token (the 16 lanes data-parallel primitives
-// exchange among), so that the instructions of a round serve four tokens.  fp64
-// keys: a wavefront per token.  Both give a lane consecutive experts.
+// exchange among), so that the instructions of a round serve four tokens; for
+// batches that leave compute units idle anyway a whole wavefront per token,
+// whose rounds are shorter (256 experts in 8 groups, one token: 5.0 against 6.2
+// us; 2048 tokens: 7.8 against 7.0).  fp64 keys: a wavefront per token.  Each
+// gives a lane consecutive experts.  What bounds it: the issue of the vector
+// units, about 300 instructions per token, and below some thousand tokens the
+// launch and the chain of rounds; 8192 tokens of 256 experts 8.7 us, 16381 of
+// 128 with a budget each 9.0 us, where their logits alone take 2 us.
 #include "moe_internal.h"
 
 namespace moe {
@@ -84,8 +90,8 @@ struct RouteArgs {
   long long part_stride;
   int32_t* ids;
   float* gates;
-  // a group: its experts, and the power of two of a row's lanes that score it;
-  // whole: the group's experts are those lanes' own (else they go through
+  // a group: its experts, and the power of two of a token's lanes that score
+  // it; whole: the group's experts are those lanes' own (else they go through
   // LDS); rows: the fp32 keys can take this grouping (at most 16 groups)
   int gs, lpg, whole, rows;
   float inv_gs;
@@ -166,6 +172,28 @@ __device__ __forceinline__ double row_sum(double v) {
   return v + dpp_d<0x121>(v);
 }
 
+// Over the 16 or 64 lanes of a token, on each of them.
+template <int TEAM>
+__device__ __forceinline__ uint32_t team_max(uint32_t v) {
+  v = row_max(v);
+  if constexpr (TEAM == 64) {
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(b[0], b[1]);
+  }
+  return v;
+}
+template <int TEAM, typename T>
+__device__ __forceinline__ T team_sum(T v) {
+  v = row_sum(v);
+  if constexpr (TEAM == 64) {
+    v += __shfl_xor(v, 16, 64);
+    v += __shfl_xor(v, 32, 64);
+  }
+  return v;
+}
+
 __device__ __forceinline__ float rank_value(uint32_t w) {
   return __uint_as_float((w & 0x80000000u) ? w ^ 0x80000000u : ~w);
 }
@@ -185,9 +213,9 @@ __device__ __forceinline__ void list_insert(uint32_t (&top)[N], uint32_t x) {
   }
 }
 
-// Zeroes the words outside the groups kept on fp32 keys; false (on the whole row)
-// where a kept group and one left out are closer than the keys' error.
-template <int EPL, int N>
+// Zeroes the words outside the groups kept on fp32 keys; false (on all lanes of
+// the token) where a kept group and one left out are closer than the keys' error.
+template <int EPL, int TEAM, int N>
 __device__ __forceinline__ bool keep_groups(uint32_t (&w)[EPL], const RouteArgs& a, uint32_t* lds, int rl, float tol) {
   uint32_t top[N];
 #pragma unroll
@@ -223,6 +251,10 @@ __device__ __forceinline__ bool keep_groups(uint32_t (&w)[EPL], const RouteArgs&
   if (a.lpg > 2) merge([](uint32_t v) { return dpp<0x4E>(v); });   // quads: lane ^ 2
   if (a.lpg > 4) merge([](uint32_t v) { return dpp<0x141>(v); });  // eights mirrored
   if (a.lpg > 8) merge([](uint32_t v) { return dpp<0x140>(v); });  // sixteens mirrored
+  if constexpr (TEAM == 64) {
+    if (a.lpg > 16) merge([](uint32_t v) { return (uint32_t)__shfl_xor((int)v, 16, 64); });
+    if (a.lpg > 32) merge([](uint32_t v) { return (uint32_t)__shfl_xor((int)v, 32, 64); });
+  }
   float total = rank_value(top[0]), size = fabsf(total);
 #pragma unroll
   for (int q = 1; q < N; ++q) {
@@ -231,30 +263,33 @@ __device__ __forceinline__ bool keep_groups(uint32_t (&w)[EPL], const RouteArgs&
       size += fabsf(rank_value(top[q]));  // keys of opposite sign: the sum's rounding follows their size
     }
   }
-  const uint32_t word = top[0] != 0u ? rank_word32(total) : 0u;  // 0: a group without an expert
-  const float most = rank_value(row_max(top[0] != 0u ? rank_word32(size) : 0u));
-  // lanes ahead of this one's group, lpg of them per group
+  const float most = rank_value(team_max<TEAM>(top[0] != 0u ? rank_word32(size) : 0u));
+  // lane g of each row takes group g's word (0: a group without an expert)
+  const int lane = threadIdx.x & 63, g16 = lane & 15;
+  uint32_t word = top[0] != 0u ? rank_word32(total) : 0u;
+  word = (uint32_t)__shfl((int)word, (TEAM == 64 ? 0 : lane & 48) + min(g16 * a.lpg, TEAM - 1), 64);
+  if (g16 >= a.G) word = 0u;
   uint32_t ahead = 0;
   auto look = [&](uint32_t o) { ahead += o > word ? 1u : 0u; };
   look(dpp<0x121>(word)), look(dpp<0x122>(word)), look(dpp<0x123>(word)), look(dpp<0x124>(word));
   look(dpp<0x125>(word)), look(dpp<0x126>(word)), look(dpp<0x127>(word)), look(dpp<0x128>(word));
   look(dpp<0x129>(word)), look(dpp<0x12A>(word)), look(dpp<0x12B>(word)), look(dpp<0x12C>(word));
   look(dpp<0x12D>(word)), look(dpp<0x12E>(word)), look(dpp<0x12F>(word));
-  const bool keep = word != 0u && ahead < (uint32_t)(a.topk_groups * a.lpg);
-  // more than topk_groups stay only among equals
-  const bool exact = row_sum(keep ? 1u : 0u) <= (uint32_t)(a.topk_groups * a.lpg);
+  const bool keep = word != 0u && ahead < (uint32_t)a.topk_groups;
+  uint32_t kept = keep ? 1u << g16 : 0u;
+  kept |= dpp<0x128>(kept);
+  kept |= dpp<0x124>(kept);
+  kept |= dpp<0x122>(kept);
+  kept |= dpp<0x121>(kept);
   const uint32_t lowest = ~row_max(keep ? ~word : 0u), left = row_max(keep ? 0u : word);
-  const bool sure =
-      exact && (left == 0u || rank_value(left) < rank_value(lowest) - a.topn * (tol + 2.4e-7f * most));
+  // (more than topk_groups stay only among equals)
+  const bool sure = __builtin_popcount(kept) <= a.topk_groups &&
+                    (left == 0u || rank_value(left) < rank_value(lowest) - a.topn * (tol + 2.4e-7f * most));
   if (a.whole) {
+    const bool mine = (kept >> ((rl / a.lpg) & 31)) & 1u;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) w[i] = keep ? w[i] : 0u;
+    for (int i = 0; i < EPL; ++i) w[i] = mine ? w[i] : 0u;
   } else {
-    uint32_t kept = keep ? 1u << (rl / a.lpg) : 0u;
-    kept |= dpp<0x128>(kept);
-    kept |= dpp<0x124>(kept);
-    kept |= dpp<0x122>(kept);
-    kept |= dpp<0x121>(kept);
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       if (!((kept >> (group_of(rl * EPL + i, a) & 31)) & 1u)) w[i] = 0u;  // (places without an expert hold 0 already)
@@ -262,8 +297,8 @@ __device__ __forceinline__ bool keep_groups(uint32_t (&w)[EPL], const RouteArgs&
   return sure;
 }
 
-// Four tokens on fp32 keys, one per row; false (nothing written) on the rows
-// that have to be routed again.  Slots whose fp32 keys are closer than their
+// Tokens on fp32 keys, one per TEAM lanes; false (nothing written) on the lanes of
+// those that have to be routed again.  Slots whose fp32 keys are closer than their
 // error are put in order by the fp64 keys of the chosen experts and of the first
 // one left out; what is left to fp64 altogether are groups that close, a third
 // expert as close to the last slot, or equal words in one lane.
@@ -275,8 +310,8 @@ __device__ __forceinline__ bool keep_groups(uint32_t (&w)[EPL], const RouteArgs&
 // by as much of the largest score, and by the 40 roundings of its sum (2.4e-6
 // of a score).  The sum with the bias adds 6e-8 of the key, and so does the difference
 // that the bound is compared through.
-template <int EPL>
-__device__ __forceinline__ bool route_rows(const RouteArgs& a, int t, int kt, uint32_t* lds, int rl,
+template <int EPL, int TEAM>
+__device__ __forceinline__ bool route_fp32(const RouteArgs& a, int t, int kt, uint32_t* lds, int rl,
                                            float* __restrict__ sum_out) {
   float v[EPL], bias[EPL], s[EPL];
   const int e0 = rl * EPL;
@@ -295,7 +330,7 @@ __device__ __forceinline__ bool route_rows(const RouteArgs& a, int t, int kt, ui
     uint32_t mw = 0u;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) mw = max(mw, avail(i) ? rank_word32(finite(v[i])) : 0u);
-    mw = row_max(mw);
+    mw = team_max<TEAM>(mw);
     m = mw ? rank_value(mw) : 0.f;
     float d = 0.f;
 #pragma unroll
@@ -303,14 +338,14 @@ __device__ __forceinline__ bool route_rows(const RouteArgs& a, int t, int kt, ui
       s[i] = avail(i) ? __expf(finite(v[i]) - m) : 0.f;
       d += s[i];
     }
-    d = row_sum(d);
+    d = team_sum<TEAM>(d);
     const float r = d > 0.f ? 1.0f / d : 0.f;
     // the largest score is r; the sum's error is common to all scores, so it moves
     // two close keys apart by no more than it moves their biases' difference
     float b = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) b = fmaxf(b, avail(i) && bias[i] < __builtin_inff() ? fabsf(bias[i]) : 0.f);
-    b = __uint_as_float(row_max(__float_as_uint(b)));
+    b = __uint_as_float(team_max<TEAM>(__float_as_uint(b)));
     tol = 5.0e-7f * r + 5.0e-6f * fminf(r, b);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) s[i] *= r;
@@ -322,26 +357,29 @@ __device__ __forceinline__ bool route_rows(const RouteArgs& a, int t, int kt, ui
   for (int i = 0; i < EPL; ++i) w[i] = avail(i) ? rank_word32(s[i] + bias[i]) : 0u;
   bool sure = true;
   if (a.G > 1)
-    sure = a.topn == 1 ? keep_groups<EPL, 1>(w, a, lds, rl, tol)
-                       : (a.topn == 2 ? keep_groups<EPL, 2>(w, a, lds, rl, tol)
-                                      : keep_groups<EPL, kMaxGroupTopn>(w, a, lds, rl, tol));
+    sure = a.topn == 1 ? keep_groups<EPL, TEAM, 1>(w, a, lds, rl, tol)
+                       : (a.topn == 2 ? keep_groups<EPL, TEAM, 2>(w, a, lds, rl, tol)
+                                      : keep_groups<EPL, TEAM, kMaxGroupTopn>(w, a, lds, rl, tol));
   uint32_t left = 0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) left += w[i] != 0u ? 1u : 0u;
-  // rounds of the four rows together, as many as the longest needs; lane j of a
-  // row keeps the j-th best expert and its word, one more than the slots where
-  // the row has a lane for it, and `after` the word that follows those
+  // rounds of the wavefront's tokens together, as many as the longest needs; lane
+  // j < 16 of a token keeps the j-th best expert and its word, one more than the
+  // slots where there is a lane for it, and `after` the word that follows those
   const int cands = min(kt + 1, 16);
   int most = cands;
-  most = max(most, __shfl_xor(most, 16, 64));
-  most = __builtin_amdgcn_readfirstlane(max(most, __shfl_xor(most, 32, 64)));
+  if constexpr (TEAM == 16) {
+    most = max(most, __shfl_xor(most, 16, 64));
+    most = max(most, __shfl_xor(most, 32, 64));
+  }
+  most = __builtin_amdgcn_readfirstlane(most);
   int my_id = -1;
   uint32_t mine = 0u, after = 0u, rounds = 0;
   for (int j = 0; j <= most; ++j) {
     uint32_t best = w[0];
 #pragma unroll
     for (int i = 1; i < EPL; ++i) best = max(best, w[i]);
-    best = row_max(best);
+    best = team_max<TEAM>(best);
     if (j == cands) after = best;
     if (j == most) break;
     uint32_t id = 0;
@@ -352,7 +390,7 @@ __device__ __forceinline__ bool route_rows(const RouteArgs& a, int t, int kt, ui
       hit[i] = w[i] == match;
       id = hit[i] ? (uint32_t)(e0 + i) : id;
     }
-    id = row_max(id);
+    id = team_max<TEAM>(id);
     const bool owner = id - (uint32_t)e0 < (uint32_t)EPL;  // of equal words one lane's go
 #pragma unroll
     for (int i = 0; i < EPL; ++i) w[i] = hit[i] && owner ? 0u : w[i];
@@ -364,7 +402,7 @@ __device__ __forceinline__ bool route_rows(const RouteArgs& a, int t, int kt, ui
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) left -= w[i] != 0u ? 1u : 0u;
-  sure = sure && row_sum(left) == rounds;  // (else a lane lost equal words)
+  sure = sure && team_sum<TEAM>(left) == rounds;  // (else a lane lost equal words)
   auto below = [&](uint32_t word, float f) { return rank_value(word) < f - (tol + 2.4e-7f * fabsf(f)); };
   const float f = rank_value(mine);
   if (rl == kt - 1 && mine != 0u && after != 0u && !below(after, f)) sure = false;
@@ -385,7 +423,7 @@ __device__ __forceinline__ bool route_rows(const RouteArgs& a, int t, int kt, ui
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       if (avail(i)) d += exp((double)finite(v[i]) - (double)m);
-    d = row_sum(d);
+    d = team_sum<TEAM>(d);
   }
   if (any_close) {  // neighbours change places where fp64 says so: even and odd pairs, then a look at all
     double key = neg_inf();
@@ -411,13 +449,13 @@ __device__ __forceinline__ bool route_rows(const RouteArgs& a, int t, int kt, ui
     const int in = (int)dpp<0x101>((uint32_t)my_id);
     if (rl < 15 && my_id >= 0 && in >= 0 && !first(key, my_id, kn, in)) sure = false;
   }
-  sure = row_max(sure ? 0u : 1u) == 0u;
+  sure = team_max<TEAM>(sure ? 0u : 1u) == 0u;
   if (rl >= kt) {  // the candidate left out
     my_id = -1;
     g = 0.0;
   }
   if (a.renorm) {
-    d = row_sum(g);
+    d = row_sum(g);  // (the slots' lanes are one row)
     g = d > 0.0 ? g / d : 0.0;
   } else if (a.score == MOE_SCORE_SOFTMAX) {
     g /= d;
@@ -573,17 +611,18 @@ __device__ __forceinline__ void route_fp64(const RouteArgs& a, int t, int kt, do
   }
 }
 
-// EPL: experts per lane of a row.  own_flags: this launch alone sets the call's
+// TEAM lanes per token, EPL experts per lane.  own_flags: this launch alone sets the call's
 // flag word -- one more block looks through every k_t -- and no launch has to
 // clear it before.
-template <int EPL>
+template <int EPL, int TEAM>
 __global__ __launch_bounds__(256) void k_route_biased(const RouteArgs a, const int32_t* __restrict__ kpt,
                                                       uint32_t* __restrict__ flags, int own_flags,
                                                       float* __restrict__ sum_out) {
-  constexpr int WPL = (EPL + 3) / 4;  // experts per lane of a wavefront
-  // fp64 keys of a token, or the words of the four rows' tokens
+  constexpr int WPL = (EPL * TEAM + 63) / 64;  // experts per lane of a wavefront
+  constexpr int TPW = 64 / TEAM;               // tokens of a wavefront
+  // fp64 keys of a token, or the words of the wavefront's tokens
   __shared__ double s_key[kWavesPerBlock][WPL * 64 > EPL * 32 ? WPL * 64 : EPL * 32];
-  const int lane = threadIdx.x & 63, rl = lane & 15;
+  const int lane = threadIdx.x & 63, rl = lane % TEAM;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (own_flags && blockIdx.x == gridDim.x - 1) {
     __shared__ int s_bad;
@@ -604,27 +643,30 @@ __global__ __launch_bounds__(256) void k_route_biased(const RouteArgs a, const i
     if (threadIdx.x == 0) *flags = s_bad ? (uint32_t)MOE_FLAG_BAD_K : 0u;
     return;
   }
-  const int t0 = (blockIdx.x * kWavesPerBlock + wave) * 4;
+  const int t0 = (blockIdx.x * kWavesPerBlock + wave) * TPW;
   if (t0 >= a.T) return;  // uniform over the wavefront; nothing below synchronises the block
 
-  // rows past the last token repeat it (the same values, written twice)
-  const int t = min(t0 + (lane >> 4), a.T - 1);
+  // lanes past the last token repeat it (the same values, written twice)
+  const int t = min(t0 + lane / TEAM, a.T - 1);
   int kt = kpt ? kpt[t] : a.k_max;
   const bool bad_k = kt < 1 || kt > a.k_max;
   if (bad_k) kt = 0;
   if (bad_k && !own_flags && rl == 0) atomicOr(flags, (uint32_t)MOE_FLAG_BAD_K);
   bool sure = false;
   if (a.rows)
-    sure = route_rows<EPL>(a, t, kt, reinterpret_cast<uint32_t*>(s_key[wave]) + (lane >> 4) * (16 * EPL), rl,
-                           sum_out);
+    sure = route_fp32<EPL, TEAM>(a, t, kt, reinterpret_cast<uint32_t*>(s_key[wave]) + (lane / TEAM) * (TEAM * EPL), rl,
+                                 sum_out);
   uint64_t again = __ballot(!sure);
   while (again) {  // tokens that fp64 has to decide
-    const int from = __builtin_ctzll(again) & ~15;
-    again &= ~(0xFFFFull << from);
+    const int from = __builtin_ctzll(again) / TEAM * TEAM;
+    again &= TEAM == 64 ? 0ull : ~(0xFFFFull << from);
     route_fp64<WPL>(a, __builtin_amdgcn_readlane(t, from), __builtin_amdgcn_readlane(kt, from), s_key[wave], lane,
                     sum_out);
   }
 }
+
+// tokens up to which each takes a whole wavefront (both sides: head of the file)
+constexpr int kWideTokens = 1024;
 
 }  // namespace
 
@@ -632,9 +674,11 @@ hipError_t launch_route_biased(const moe_shape& s, const float* logits, const fl
                                const int32_t* k_per_token, int32_t* ids, float* gates, uint32_t* flags,
                                bool own_flags, hipStream_t st, int parts, long long part_stride, float* sum_out) {
   const int E = s.num_experts;
-  const int grid = (s.num_tokens + 4 * kWavesPerBlock - 1) / (4 * kWavesPerBlock);
-  int epl = 1;  // experts per lane of a row
-  while (16 * epl < E) epl *= 2;
+  const int team = s.num_tokens <= kWideTokens ? 64 : 16;
+  const int per_block = 64 / team * kWavesPerBlock;
+  const int grid = (s.num_tokens + per_block - 1) / per_block;
+  int epl = 1;  // experts per lane of a token
+  while (team * epl < E) epl *= 2;
   RouteArgs a{};
   a.logits = logits;
   a.select_bias = select_bias;
@@ -655,22 +699,31 @@ hipError_t launch_route_biased(const moe_shape& s, const float* logits, const fl
   a.inv_gs = 1.0f / (float)a.gs;
   const int own = a.gs / epl;
   a.whole = a.gs % epl == 0 && (own & (own - 1)) == 0;
-  a.lpg = 16;
-  while (a.lpg * a.G > 16 && a.lpg > 1) a.lpg >>= 1;
+  a.lpg = team;
+  while (a.lpg * a.G > team && a.lpg > 1) a.lpg >>= 1;
   if (a.whole) a.lpg = own;
   a.rows = a.G <= 16;
   const auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   a.vec = E % 4 == 0 && aligned(logits) && aligned(select_bias);
-#define MOE_ROUTE_LAUNCH(EPL)                                                                       \
-  hipLaunchKernelGGL(k_route_biased<EPL>, dim3(grid + (own_flags ? 1 : 0)), dim3(256), 0, st, a, k_per_token, flags,      \
-                     own_flags ? 1 : 0, sum_out)
-  switch (epl) {
-    case 1: MOE_ROUTE_LAUNCH(1); break;
-    case 2: MOE_ROUTE_LAUNCH(2); break;
-    case 4: MOE_ROUTE_LAUNCH(4); break;
-    case 8: MOE_ROUTE_LAUNCH(8); break;
-    case 16: MOE_ROUTE_LAUNCH(16); break;
-    default: MOE_ROUTE_LAUNCH(32); break;
+#define MOE_ROUTE_LAUNCH(EPL, TEAM)                                                                              \
+  hipLaunchKernelGGL((k_route_biased<EPL, TEAM>), dim3(grid + (own_flags ? 1 : 0)), dim3(256), 0, st, a,          \
+                     k_per_token, flags, own_flags ? 1 : 0, sum_out)
+  if (team == 64) {
+    switch (epl) {
+      case 1: MOE_ROUTE_LAUNCH(1, 64); break;
+      case 2: MOE_ROUTE_LAUNCH(2, 64); break;
+      case 4: MOE_ROUTE_LAUNCH(4, 64); break;
+      default: MOE_ROUTE_LAUNCH(8, 64); break;
+    }
+  } else {
+    switch (epl) {
+      case 1: MOE_ROUTE_LAUNCH(1, 16); break;
+      case 2: MOE_ROUTE_LAUNCH(2, 16); break;
+      case 4: MOE_ROUTE_LAUNCH(4, 16); break;
+      case 8: MOE_ROUTE_LAUNCH(8, 16); break;
+      case 16: MOE_ROUTE_LAUNCH(16, 16); break;
+      default: MOE_ROUTE_LAUNCH(32, 16); break;
+    }
   }
 #undef MOE_ROUTE_LAUNCH
   return hipGetLastError();

@@ -39,6 +39,14 @@ def check(logits, bias, k, kpt=None, **o):
     want, w = P.route_biased(logits, bias, k, kpt, **o)
     assert np.array_equal(ids, want), np.nonzero((ids != want).any(1))[0][:5]
     assert np.all(np.abs(gates - w) <= (P.U32 + 1e-13) * np.abs(w) + 1e-45)
+    # many tokens share wavefronts, few have one each: the same tokens in a large and odd batch (the fp64 sums of
+    # gates may be formed in another order)
+    T = len(logits)
+    if T <= 1024:
+        n = 1027 // T + 1
+        many, g2, f2 = route(np.tile(logits, (n, 1)), bias, k, None if kpt is None else np.tile(kpt, n), **o)
+        assert np.array_equal(many, np.tile(ids, (n, 1))) and f2 == flags
+        assert np.all(np.abs(g2 - np.tile(w, (n, 1))) <= (P.U32 + 1e-13) * np.abs(np.tile(w, (n, 1))) + 1e-45)
     return ids, gates, flags
 
 
