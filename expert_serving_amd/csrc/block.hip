@@ -95,6 +95,17 @@ __device__ __forceinline__ void store_stream(void* p, bool bf16, size_t i, const
   }
 }
 
+// Blocks of one row each in a grid whose first axis stays below 2^32 threads.
+constexpr int kGridRows = 1 << 21;
+inline dim3 row_grid(int rows) {
+  return dim3(rows < kGridRows ? rows : kGridRows, (unsigned)(((long long)rows + kGridRows - 1) / kGridRows));
+}
+// this block's row, from kGridRows * blockIdx.y; at or past the last in the rest of a grid's last line
+__device__ __forceinline__ int grid_row() {
+  const uint32_t r = blockIdx.y * (uint32_t)kGridRows + blockIdx.x;
+  return r < 0x7FFFFFFFu ? (int)r : 0x7FFFFFFF;
+}
+
 // Sum and maximum over the block, in a fixed order, on every thread.
 template <int NT>
 __device__ __forceinline__ void block_sum_max(float& sum, float& top) {
@@ -125,13 +136,13 @@ __device__ __forceinline__ void block_sum_max(float& sum, float& top) {
 // codes), one reduction gives both the sum of squares and the row's maximum.
 // NORM false: quantisation of x itself.
 template <int DT, int V, int NT, bool NORM>
-__global__ __launch_bounds__(NT) void k_rows(int cols, const void* x, const float* __restrict__ weight, float eps,
+__global__ __launch_bounds__(NT) void k_rows(int rows, int cols, const void* x, const float* __restrict__ weight, float eps,
                                              int out_bf16, void* out, uint8_t* __restrict__ codes,
                                              float* __restrict__ scales, const int32_t* __restrict__ rows_dev,
                                              uint32_t* __restrict__ h_flags) {
   constexpr int G = granule(DT);
-  const int r = blockIdx.x;
-  if (rows_dev && r >= *rows_dev) return;  // uniform over the block
+  const int r = grid_row();
+  if (r >= (rows_dev ? min(rows, *rows_dev) : rows)) return;  // uniform over the block
   const int granules = cols / G;
   const size_t base = (size_t)r * cols;
   float t[V > 0 ? V : 1][G];
@@ -214,7 +225,7 @@ hipError_t launch_rows(int rows, int cols, const void* x, const float* weight, f
   if (rows <= 0) return hipSuccess;
   const int granules = cols / granule(DT);
 #define MOE_ROWS(V, NT)                                                                                      \
-  hipLaunchKernelGGL((k_rows<DT, V, NT, NORM>), dim3(rows), dim3(NT), 0, st, cols, x, weight, eps,           \
+  hipLaunchKernelGGL((k_rows<DT, V, NT, NORM>), row_grid(rows), dim3(NT), 0, st, rows, cols, x, weight, eps, \
                      out_dtype == MOE_BF16 ? 1 : 0, out, static_cast<uint8_t*>(codes), scales, rows_dev, h_flags)
   // many short rows to quantise: a wavefront each, without the block's barrier
   // (65536 rows of 1024 fp16 39 against 58 us, of 2048 85 against 91); fewer or
@@ -261,10 +272,11 @@ template <int DT, int KM, int V, int NT>
 __global__ __launch_bounds__(NT) void k_combine_norm(const void* __restrict__ y, int parts, long long part_stride,
                                                      const int32_t* __restrict__ row_of_slot,
                                                      const float* __restrict__ gates,
-                                                     const void* __restrict__ shared, int H, int k_max,
+                                                     const void* __restrict__ shared, int T, int H, int k_max,
                                                      const BlockEnd e) {
   constexpr int G = granule(DT);
-  const int t = blockIdx.x;
+  const int t = grid_row();
+  if (t >= T) return;
   // the token's slots, uniform over the block (scalar registers).  A slot
   // without a row loads the row of a slot that has one (from the cache) and
   // masks it to zeros, so that no load waits behind a branch
@@ -381,8 +393,8 @@ hipError_t launch_end(const moe_shape& s, const void* y, const int32_t* row_of_s
                       const void* shared, const BlockEnd& e, hipStream_t st, int parts, long long part_stride) {
   const int granules = s.hidden / granule(DT);
 #define MOE_END(V, NT)                                                                                       \
-  hipLaunchKernelGGL((k_combine_norm<DT, KM, V, NT>), dim3(s.num_tokens), dim3(NT), 0, st, y, parts,         \
-                     part_stride, row_of_slot, gates, shared, s.hidden, s.top_k, e)
+  hipLaunchKernelGGL((k_combine_norm<DT, KM, V, NT>), row_grid(s.num_tokens), dim3(NT), 0, st, y, parts,     \
+                     part_stride, row_of_slot, gates, shared, s.num_tokens, s.hidden, s.top_k, e)
   if (granules <= 256) MOE_END(1, 256);
   else if (granules <= 512) MOE_END(2, 256);
   else if (granules <= 1024) MOE_END(4, 256);

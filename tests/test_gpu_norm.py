@@ -161,3 +161,29 @@ def test_residual_scale_of_zero_reads_no_residual():
     abi.moe_combine_norm(shape, abi.make_block(residual_scale=0.0, stream_dtype=abi.MOE_F32), abi.MOE_F32,
                          randn(1, T, H), rows, torch.ones(T, k, device=dev()), None, res, out)
     assert torch.isfinite(out).all()
+
+
+def test_more_rows_than_one_axis_of_a_launch_holds():
+    """Blocks of a row each, with 2^32 threads and more."""
+    rows = 70_000_000
+    x = torch.ones(rows, 128, device=dev(), dtype=torch.bfloat16)
+    x[-1] = torch.linspace(-3, 3, 128, device=dev()).to(torch.bfloat16)
+    codes, scales = abi.quantize_int8(x)
+    assert np.array_equal(codes[-1].cpu().numpy(), P.codes(np64(x[-1:]))[0][0])
+    assert bool((codes[:-1:65_521] == 127).all()) and int(codes[-2].sum()) == 127 * 128
+    assert float(scales[-2]) == np.float32(1) / np.float32(127)
+    del codes, scales
+    want = P.rms_norm(np64(x[-1:]), None, 1e-5)
+    abi.moe_norm(rows, 128, abi.MOE_BF16, x, None, 1e-5, abi.MOE_BF16, x, None, None)
+    assert np.all(np.abs(np64(x[-1:]) - want) <= (P.UB16 + 50 * P.U32) * np.abs(want))
+    assert bool((x[:-1:65_521] == 1).all()) and bool((x[-2] == 1).all())
+    del x
+    T, H = 17_000_000, 64
+    shape = abi.make_shape(num_tokens=T, hidden=H, num_experts=1, intermediate=64, top_k=1)
+    y = torch.ones(T, H, device=dev(), dtype=torch.bfloat16)
+    ros, g = torch.arange(T, device=dev(), dtype=torch.int32).view(T, 1), torch.ones(T, 1, device=dev())
+    g[-1], g[-2] = 3.0, 2.0
+    res = torch.ones(T, H, device=dev(), dtype=torch.bfloat16)
+    abi.moe_combine_norm(shape, abi.make_block(residual_scale=1.0, stream_dtype=abi.MOE_BF16), abi.MOE_BF16, y, ros, g,
+                         None, res, res)
+    assert bool((res[-1] == 4).all()) and bool((res[-2] == 3).all()) and bool((res[:-2:4_099] == 2).all())
