@@ -8,6 +8,10 @@
 // block takes one row; a thread owns granules of 16 loaded bytes (8 values of 2
 // bytes, 4 of 4), granule g of the row in thread g % NT, V of them per thread.
 // Rows too long for that (V = 0) are read a second time.
+// Measured: norm of 8192 x 7168 fp32 to bf16 and codes 79.7 us (352 MB, 4.4 TB/s,
+// a device copy 4.7), 65536 x 1024 fp16 to codes 39 us; combine of 8192 x 7168,
+// eight slots and a shared expert, with norm, gate and residual 282 us (1.39 GB,
+// 4.9 TB/s); 64 rows of 4096 in 4.9 us, of which the launch takes 4.7.
 #include "moe_internal.h"
 #include "quant_int8.h"
 
