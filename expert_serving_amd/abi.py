@@ -390,8 +390,11 @@ def moe_quantize_int8(rows, cols, src_dtype, src, codes, scales, stream=None):
 
 
 def quantize_int8(t, stream=None):
-    """(codes int8 of t's shape, scales fp32 of its leading dimensions) of a bf16, fp32 or fp16 device tensor."""
+    """(codes int8 of t's shape, scales fp32 of its leading dimensions) of a bf16, fp32 or fp16 device tensor
+    (contiguous when a stream is given: a copy of it would be made on torch's current stream)."""
     import torch
+    if stream is not None and not t.is_contiguous():
+        raise ValueError("a tensor quantised on a given stream has to be contiguous")
     dt = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}[t.dtype]
     codes = torch.empty(t.shape, dtype=torch.int8, device=t.device)
     scales = torch.empty(t.shape[:-1], dtype=torch.float32, device=t.device)
@@ -448,6 +451,8 @@ def make_block(select_bias=None, pre_norm=None, post_norm=None, eps=1e-6, gate=N
                  0, 0, MOE_F32, int(stream_dtype))
     if gate is not None:
         import torch
+        if gate.dim() not in (1, 2):
+            raise ValueError("the gate has one or two dimensions")
         rows, cols = gate.shape if gate.dim() == 2 else (1, gate.shape[0])
         if cols > 1 and gate.stride(-1) not in (0, 1):
             raise ValueError("the gate's columns have to be one element apart")

@@ -69,11 +69,12 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 /* device flag bits (moe_read_device_flags) */
 #define MOE_FLAG_BAD_K 1u       /* some k_per_token[t] outside [1, top_k]: token routed nowhere */
 #define MOE_FLAG_BAD_EXPERT 2u  /* some topk_ids entry outside [-1, E): slot treated as unused  */
-#define MOE_FLAG_H_RANGE 4u     /* some SwiGLU activation h exceeded fp16 range (bf16 layers)
-                                   or was not finite (MXFP8 layers)                           */
+#define MOE_FLAG_H_RANGE 4u     /* some SwiGLU activation h exceeded fp16 range (bf16 and int8
+                                   experts) or was not finite (MXFP8 experts)                 */
 #define MOE_FLAG_BAD_REPLICA 8u /* a routed expert without a replica, or a replica id out of range */
 #define MOE_FLAG_Y_RANGE 16u    /* some expert output exceeded fp16 range inside a layer call
-                                   (moe_layer_forward, moe_layer_forward_mxfp8)                */
+                                   (moe_layer_forward, moe_layer_forward_mxfp8), a block call or
+                                   an fp16 y of the int8 calls                                 */
 
 typedef struct {
   int32_t num_tokens;          /* T >= 0                                                  */

@@ -209,3 +209,12 @@ def test_gate_strides_of_the_binding():
         abi.make_block(gate=torch.zeros(T, 2 * H)[:, ::2])
     with pytest.raises(KeyError):
         abi.make_block(gate=torch.zeros(H, dtype=torch.float16))
+    for dims in ((), (1, T, H)):
+        with pytest.raises(ValueError):
+            abi.make_block(gate=torch.zeros(dims))
+
+
+def test_strided_tensors_are_not_quantised_on_another_stream():
+    import torch
+    with pytest.raises(ValueError):
+        abi.quantize_int8(torch.zeros(128, 128).t(), stream=1)

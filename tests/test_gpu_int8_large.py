@@ -197,3 +197,19 @@ def test_int8_block(name):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("offsets", [False, True])
+def test_rows_and_outputs_past_32_bit_offsets(offsets):
+    """More than 2^31 codes of rows, and more than 2^31 outputs."""
+    for rows, N, K in ((600_001, 16, 4096), (300_001, 8192, 128)):
+        a = torch.ones(rows, K, dtype=torch.int8, device=dev())
+        a[-1], a[-2] = 3, 2
+        w = torch.ones(1, N, K, dtype=torch.int8, device=dev())
+        w[0, -1] = -1
+        off = torch.tensor([0, rows], dtype=torch.int32, device=dev()) if offsets else None
+        y, flags = product(a, torch.ones(rows, device=dev()), off, w, torch.ones(1, N, device=dev()), "bf16")
+        for r, f in ((0, 1), (rows // 2, 1), (rows - 3, 1), (rows - 2, 2), (rows - 1, 3)):
+            assert bool((y[r, :-1] == f * K).all()) and float(y[r, -1]) == -f * K, (rows, r)
+        assert flags == 0
+        del a, w, y
