@@ -1329,32 +1329,44 @@ __global__ __launch_bounds__(512) void k_gemm_mfma2(
 // Measured on the FFN of 65536 rows over 256 experts (60 to 800 rows each): 256-row
 // tiles with 64-row ones for short rests, eight row tiles by column, 4.46 ms;
 // heights by rows, one row tile after the other 4.07 ms.
-template <int BNB, int MODE>
+// HALVES: a tile is taken as two of up to 128 rows; blocks of 128 columns then
+// fit a compute unit twice (93 VGPRs, 64 KB of LDS).
+template <int BNB, int MODE, bool HALVES>
 __global__ __launch_bounds__(512) void k_gemm_rows_i8(
     const uint16_t* __restrict__ A, const int32_t* __restrict__ a_rows, int lda, const uint16_t* __restrict__ B0,
     const uint16_t* __restrict__ B1, long long strideB, int N, int K, void* __restrict__ Out, int ldo,
     uint32_t* __restrict__ flags, const MxArgs mx, const MTile* __restrict__ sched,
     const int32_t* __restrict__ count, int mslots, int ntiles, int ksplit, long long part_elems) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
-  const int cols = ntiles * ksplit;
+  const int cols = ntiles * ksplit * (HALVES ? 2 : 1);
   int L;
   if (!xcd_index(min(*count, mslots) * cols, L)) return;
   const int at = L / cols;  // a tile of the group that L falls in
   const int group = sched[at].group, first = at - (group & 0xFF), size = group >> 8;
-  const int r = L - first * cols, nn = r / size, mi = first + (r - nn * size);
-  const int rows = sched[mi].rows;
-  if (rows <= 0) return;
+  const int r = L - first * cols, col = r / size;
+  MTile t = sched[first + (r - col * size)];
+  int nn = col;
+  if constexpr (HALVES) {
+    nn = col >> 1;
+    t.row0 += 128 * (col & 1);
+    t.rows = min(t.rows - 128 * (col & 1), 128);
+  }
+  if (t.rows <= 0) return;
   const int part = nn % ksplit, ni = nn / ksplit;
   const int stages = K / kPingRowElems;
   const int kst0 = part * stages / ksplit, kstn = (part + 1) * stages / ksplit - kst0;
   if (part) Out = static_cast<float*>(Out) + part * part_elems;
 #define MOE_ROWS_I8(BM)                                                                                        \
-  gemm_tile<BM, BNB, MODE, 2, 8>(smem, A, a_rows, lda, B0, B1, strideB, N, K, Out, ldo, nullptr, sched, 0, flags, mx, \
-                                 mi, ni, kst0, kstn)
-  if (rows <= 64) MOE_ROWS_I8(64);
-  else if (rows <= 128) MOE_ROWS_I8(128);
-  else if (rows <= 192) MOE_ROWS_I8(192);
-  else MOE_ROWS_I8(256);
+  gemm_tile<BM, BNB, MODE, 2, 8>(smem, A, a_rows, lda, B0, B1, strideB, N, K, Out, ldo, nullptr, &t, 0, flags, mx, 0, \
+                                 ni, kst0, kstn)
+  if (t.rows <= 64) {
+    MOE_ROWS_I8(64);
+  } else if (HALVES || t.rows <= 128) {
+    MOE_ROWS_I8(128);
+  } else if constexpr (!HALVES) {
+    if (t.rows <= 192) MOE_ROWS_I8(192);
+    else MOE_ROWS_I8(256);
+  }
 #undef MOE_ROWS_I8
 }
 
@@ -1602,18 +1614,19 @@ hipError_t launch_mfma2(const void* A, const int32_t* a_rows, int lda, const voi
   return hipGetLastError();
 }
 
-template <int BNB, int MODE>
+template <int BNB, int MODE, bool HALVES>
 hipError_t launch_rows_i8(const void* A, const int32_t* a_rows, const void* B0, const void* B1, int N, int K,
                           void* out, const MTile* sched, const int32_t* count, int mslots, uint32_t* flags,
                           hipStream_t st, const MxArgs mx, int ksplit, long long part_elems) {
   if (mslots == 0) return hipSuccess;
-  constexpr int lds = gemm_lds_bytes(256, BNB, MODE, 2, 8);
+  constexpr int lds = gemm_lds_bytes(HALVES ? 128 : 256, BNB, MODE, 2, 8);
   static_assert(lds <= 160 * 1024, "LDS");
   static std::atomic<uint64_t> set_on{0};
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(&k_gemm_rows_i8<BNB, MODE>), lds, set_on);
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(&k_gemm_rows_i8<BNB, MODE, HALVES>), lds, set_on);
   if (e != hipSuccess) return e;
   const int ntiles = (N + BNB - 1) / BNB, K2 = K / 2;  // K in 16-bit units
-  hipLaunchKernelGGL((k_gemm_rows_i8<BNB, MODE>), dim3(grid_for(mslots, ntiles * ksplit)), dim3(512), lds, st,
+  const dim3 grid(grid_for(mslots, ntiles * ksplit * (HALVES ? 2 : 1)));
+  hipLaunchKernelGGL((k_gemm_rows_i8<BNB, MODE, HALVES>), grid, dim3(512), lds, st,
                      static_cast<const uint16_t*>(A), a_rows, K2, static_cast<const uint16_t*>(B0),
                      static_cast<const uint16_t*>(B1), (long long)N * K2, N, K2, out, N, flags, mx, sched, count, mslots,
                      ntiles, ksplit, part_elems);
@@ -1969,17 +1982,20 @@ hipError_t launch_gemm_gateup_i8_rows(const void* A, const int32_t* a_rows, cons
                                       hipStream_t st) {
   const MxArgs mx{reinterpret_cast<const uint8_t*>(sa), reinterpret_cast<const uint8_t*>(sbg),
                   reinterpret_cast<const uint8_t*>(sbu), nullptr, 0, 0, 0, 0};
-  return launch_rows_i8<128, kGateUpI8>(A, a_rows, Bg, Bu, N, K, h, sched, count, max_tiles, flags, st, mx, 1, 0);
+  return launch_rows_i8<128, kGateUpI8, false>(A, a_rows, Bg, Bu, N, K, h, sched, count, max_tiles, flags, st, mx, 1, 0);
 }
 
 hipError_t launch_gemm_down_i8_rows(const void* A, const float* sa, const void* B, const float* sb, int N, int K,
                                     int y_dtype, void* Y, const MTile* sched, const int32_t* count, int max_tiles,
-                                    uint32_t* flags, hipStream_t st, int ksplit, long long part_elems) {
+                                    bool halves, uint32_t* flags, hipStream_t st, int ksplit, long long part_elems) {
   if (ksplit > 1 && y_dtype != MOE_F32) return hipErrorInvalidValue;
   const MxArgs mx{reinterpret_cast<const uint8_t*>(sa), reinterpret_cast<const uint8_t*>(sb), nullptr, nullptr, 0,
                   0, y_dtype, 0};
-  return launch_rows_i8<256, kDownI8>(A, nullptr, B, nullptr, N, K, Y, sched, count, max_tiles, flags, st, mx, ksplit,
-                                      part_elems);
+  if (halves)
+    return launch_rows_i8<128, kDownI8, true>(A, nullptr, B, nullptr, N, K, Y, sched, count, max_tiles, flags, st, mx,
+                                              ksplit, part_elems);
+  return launch_rows_i8<256, kDownI8, false>(A, nullptr, B, nullptr, N, K, Y, sched, count, max_tiles, flags, st, mx,
+                                             ksplit, part_elems);
 }
 
 }  // namespace moe

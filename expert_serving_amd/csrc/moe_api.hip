@@ -354,6 +354,18 @@ bool stream_i8(const GemmPlan& gp, const moe_shape& s, int max_small, long long 
   return !gp.has_big() && stream_tiles(s, max_small) * matrix_bytes <= kStreamMaxBytes;
 }
 
+// int8 products whose 256 x 256 tiles (about half an expert's worth more than
+// the rows fill) would leave half the compute units idle run on 128 x 128 ones.
+// Measured, 256 against 128: 1024 rows x 4096 x 4096 (80 tiles) 51 against 32 us,
+// the down projection of 3738 rows over 14 experts, 640 x 4864 (63), 59 against
+// 36; 2000 rows x 4096 x 4096 (128) 57 against 54, 3000 rows (192) 63 against 84,
+// 3000 rows over 16 experts, 2048 x 2048 (152), 35 against 38.  The gate/up
+// product of as few tiles is slower on halves (5364 rows, 768 x 768: 22 against 27).
+bool few_tiles_i8(const moe_shape& s, int n) {
+  const long long slots = (long long)s.num_tokens * s.top_k;
+  return (slots / 256 + (s.num_experts + 1) / 2) * ((n + 255) / 256) < kComputeUnits / 2;
+}
+
 // The second product of a batch of few and short rows quantises them itself:
 // every block passes over its tile's rows (at most 16) where a launch would
 // pass over them once.
@@ -672,8 +684,10 @@ moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows,
     return MOE_OK;
   }
   // (the down projection has the fewer column tiles, so the fewer rounds)
+  const bool halves = ksplit == 1 && few_tiles_i8(s, H);
   MOE_HIP(launch_build_schedule(offsets, E, gp, sb, L.max_tiles_big, ss, L.max_tiles_small, cnt, st,
-                                clear_flags ? flags : nullptr, gp.has_big() && ksplit == 1 ? (H + 255) / 256 : 0));
+                                clear_flags ? flags : nullptr,
+                                gp.has_big() && ksplit == 1 && !halves ? (H + 255) / 256 : 0));
   MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, true, st));
   if (gp.has_big()) {
     MOE_HIP(launch_gemm_gateup_i8_rows(xq, a_rows, xsc, w.gate, w.gate_scales, w.up, w.up_scales, I, H, h, sb, cnt,
@@ -694,8 +708,8 @@ moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows,
   MOE_HIP(stage_mark(dbg, MOE_STAGE_DOWN, true, st));
   const long long pe = (long long)slots * H;
   if (gp.has_big())
-    MOE_HIP(launch_gemm_down_i8_rows(hq, hsc, w.down, w.down_scales, H, I, y_dtype, y, sb, cnt, L.max_tiles_big, flags,
-                                     st, ksplit, pe));
+    MOE_HIP(launch_gemm_down_i8_rows(hq, hsc, w.down, w.down_scales, H, I, y_dtype, y, sb, cnt, L.max_tiles_big, halves,
+                                     flags, st, ksplit, pe));
   else
     MOE_HIP(launch_gemm_down_i8(gp.bm_small, hq, hsc, w.down, w.down_scales, H, I, y_dtype, y, ss, cnt + 1,
                                 L.max_tiles_small, 0, flags, st, ksplit, pe));
@@ -1476,11 +1490,12 @@ moe_status moe_grouped_gemm_int8(int32_t rows, int32_t n, int32_t k, int32_t num
     MOE_HIP(launch_gemm_down_i8(bm, a, a_scales, b, b_scales, n, k, dt, dst, nullptr, nullptr, 0, rows, flags, st,
                                 p.ksplit, pe));
   } else {
+    const bool halves = !split && few_tiles_i8(p.s, n);
     MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sb, p.max_big, ss, p.max_small, cnt, st, flags,
-                                  p.gp.has_big() && !split ? (n + 255) / 256 : 0));
+                                  p.gp.has_big() && !split && !halves ? (n + 255) / 256 : 0));
     if (p.gp.has_big())
-      MOE_HIP(launch_gemm_down_i8_rows(a, a_scales, b, b_scales, n, k, dt, dst, sb, cnt, p.max_big, flags, st, p.ksplit,
-                                       pe));
+      MOE_HIP(launch_gemm_down_i8_rows(a, a_scales, b, b_scales, n, k, dt, dst, sb, cnt, p.max_big, halves, flags, st,
+                                       p.ksplit, pe));
     else
       MOE_HIP(launch_gemm_down_i8(p.gp.bm_small, a, a_scales, b, b_scales, n, k, dt, dst, ss, cnt + 1, p.max_small,
                                   0, flags, st, p.ksplit, pe));

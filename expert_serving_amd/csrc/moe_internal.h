@@ -272,14 +272,16 @@ hipError_t launch_gemm_down_i8(int bm, const void* A, const float* sa, const voi
                                int y_dtype, void* Y, const MTile* sched, const int32_t* count, int max_tiles,
                                int static_rows, uint32_t* flags, hipStream_t st, int ksplit = 1,
                                long long part_elems = 0);
-// row tiles of up to 256 rows, each at the height its rows need
+// row tiles of up to 256 rows, each at the height its rows need; halves: as two
+// of up to 128, on tiles of 128 columns instead of 256
 hipError_t launch_gemm_gateup_i8_rows(const void* A, const int32_t* a_rows, const float* sa, const void* Bg,
                                       const float* sbg, const void* Bu, const float* sbu, int N, int K, void* h,
                                       const MTile* sched, const int32_t* count, int max_tiles, uint32_t* flags,
                                       hipStream_t st);
 hipError_t launch_gemm_down_i8_rows(const void* A, const float* sa, const void* B, const float* sb, int N, int K,
                                     int y_dtype, void* Y, const MTile* sched, const int32_t* count, int max_tiles,
-                                    uint32_t* flags, hipStream_t st, int ksplit = 1, long long part_elems = 0);
+                                    bool halves, uint32_t* flags, hipStream_t st, int ksplit = 1,
+                                    long long part_elems = 0);
 // The products of few rows (stream_i8.hip).  offsets [E + 1] (null: rows [0,
 // static_rows) of one expert); max_tiles bounds the 32-row tiles, max_rows the
 // rows of an expert.  clear_flags: the launch first clears the flag word (it
