@@ -224,14 +224,23 @@ GemmPlan choose_gemm_plan(const moe_shape& s) {
   return p;
 }
 
-// int8 products: 32-row tiles below 64 rows per expert, else tiles of up to 256
-// rows that run at the height of their rows (no small class).
-GemmPlan choose_gemm_plan_i8(const moe_shape& s) {
-  GemmPlan p = choose_gemm_plan(s);
-  if (p.has_big()) {
-    p.split_rows = 0;
-    p.tail_rows = 0;
-  }
+// int8 products: 32-row tiles (streams need them), or tiles of up to 256 rows
+// that run at the height of their rows (no small class).  The latter read an
+// expert's weights once where it has 16 rows and more on average (one expert of
+// all rows: 64, so that the call without offsets is planned alike), and few rows of
+// many experts fill the compute units without the splits of K that 32-row tiles
+// of few experts have.  FFNs on 32-row tiles against tiles of up to 256: 16
+// rows each, 8 experts of 4096 x 14336, 274 against 262 us, 40
+// rows 356 against 295; 12 rows 230 against 257; 64 experts of 2048 x 1408, 6
+// rows 120 against 112, 60 rows 192 against 133; 256 of 7168 x 2048, 3 rows 1684
+// against 1714, 60 rows 3382 against 2177.
+GemmPlan choose_gemm_plan_i8(const moe_shape& s, bool stream) {
+  const long long avg = (long long)s.num_tokens * s.top_k / s.num_experts;
+  GemmPlan p;
+  p.bm_big = 256;
+  p.bm_small = 32;
+  p.tail_rows = 0;
+  p.split_rows = !stream && (avg >= (s.num_experts > 1 ? 16 : 64) || (avg >= 3 && s.num_experts >= 64)) ? 0 : 0x7fffffff;
   return p;
 }
 
@@ -335,24 +344,31 @@ int gate_up_parts(long long blocks, int stages, bool rounds) {
   return best;
 }
 
-// Row tiles of a plan without big tiles: each expert that has rows ends with
-// one tile that may be short.
-int stream_tiles(const moe_shape& s, int max_small) {
+// 32-row tiles of the slots: each expert that has rows ends with one that may be
+// short.
+long long stream_tiles(const moe_shape& s) {
   const long long slots = (long long)s.num_tokens * s.top_k;
-  return (int)std::min<long long>(max_small, std::min<long long>(slots, s.num_experts) + slots / 32);
+  return std::min<long long>(slots, s.num_experts) + slots / 32;
 }
 
-// int8 products of small row tiles stream their weights (launch_stream_i8)
-// while the tiles together read at most this; above it the LDS tiles come nearer
-// to the memory's rate.  Measured, streams against LDS tiles: FFN of 1 token
-// over 128 experts (36 MB) 14.9 against 32.0 us, of 4 tokens (144 MB) 42 against
-// 50, of 16 (576 MB) 104 against 78, of 1 token over 256 larger experts (336 MB)
-// 87 against 77; products of 8 rows of 224 MB 50 against 53 us, of 60 rows (two
-// tiles, 448 MB) 104 against 71.
-constexpr long long kStreamMaxBytes = 240LL << 20;
-bool stream_i8(const GemmPlan& gp, const moe_shape& s, int max_small, long long matrix_bytes) {
-  return !gp.has_big() && stream_tiles(s, max_small) * matrix_bytes <= kStreamMaxBytes;
+// int8 products of fewer than 64 rows per expert stream their weights
+// (launch_stream_i8) while the 32-row tiles together read at most 240 MB, and at
+// most 120 KB per k of their (mean) K: above it the LDS tiles come nearer to the
+// memory's rate, and the wavefronts of a stream, which share K, have too little of
+// a short one.  Measured, streams against LDS tiles: FFN of 1 token over 128
+// experts (36 MB) 14.9 against 32.0 us, of 4 tokens (144 MB) 42 against 50, of 16
+// (576 MB) 104 against 78, of 1 token over 256 larger experts (336 MB) 87 against
+// 77; 60 rows x 28672 x 8192 (448 MB) 104 against 71; FFN of 1024 x 1024, 16
+// experts, 84 MB 28 against 29, 138 MB 42 against 33; of 2048 x 2048, 8 experts,
+// 168 MB 38 against 41, 216 MB 47 against 45; of 640 x 384, 64 experts, 62 MB 27
+// against 31, 79 MB 32 against 31; product of 1024 x 512, 128 experts,
+// 70 MB 28 against 23; of 304 x 4480, 49 experts, 143 MB 32 against 39.
+bool stream_i8(const moe_shape& s, long long matrix_bytes, long long mean_k) {
+  if ((long long)s.num_tokens * s.top_k / s.num_experts >= 64) return false;
+  return stream_tiles(s) * matrix_bytes <= std::min(240LL << 20, mean_k * (120LL << 10));
 }
+// of an FFN whose gate, up and down matrices a tile reads
+bool stream_ffn_i8(const moe_shape& s, long long H, long long I) { return stream_i8(s, 3 * H * I, (2 * H + I) / 3); }
 
 // int8 products whose 256 x 256 tiles (about half an expert's worth more than
 // the rows fill) would leave half the compute units idle run on 128 x 128 ones.
@@ -380,7 +396,8 @@ WsLayout plan_workspace(const moe_shape& s, int format, bool normed) {
   const size_t H = (size_t)s.hidden, I = (size_t)s.intermediate, Is = (size_t)s.shared_intermediate;
   const size_t eb = mx ? 1 : (size_t)elem_bytes(s.act_dtype);  // bytes of an h element
   const size_t slots = T * k;
-  const GemmPlan gp = i8 ? choose_gemm_plan_i8(s) : choose_gemm_plan(s);
+  w.stream = i8 && stream_ffn_i8(s, s.hidden, s.intermediate);
+  const GemmPlan gp = i8 ? choose_gemm_plan_i8(s, w.stream) : choose_gemm_plan(s);
   w.n_dispatch_tiles = (int)((slots + kDispatchTileSlots - 1) / kDispatchTileSlots);
   tile_bounds(s, gp, w.max_tiles_big, w.max_tiles_small);
   w.ksplit = down_parts(s, gp, w.max_tiles_small, mx || i8);
@@ -398,9 +415,10 @@ WsLayout plan_workspace(const moe_shape& s, int format, bool normed) {
   }
   if (i8) {
     if (gp.has_big()) w.max_tiles_big += kUnits;  // (cut tiles)
-    w.stream = stream_i8(gp, s, w.max_tiles_small, 3LL * (long long)(H * I));
     // the shared expert: a batch whose every row takes one expert
-    w.stream_shared = Is > 0 && T < 64 && (long long)((T + 31) / 32 * 3 * H * Is) <= kStreamMaxBytes;
+    moe_shape one = s;
+    one.num_experts = one.top_k = 1;
+    w.stream_shared = Is > 0 && stream_ffn_i8(one, s.hidden, s.shared_intermediate);
     if (w.stream) w.ksplit = w.ks_gu = 1;
     if (w.stream_shared) w.ks_gus = 1;
   }
@@ -659,7 +677,7 @@ moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows,
                       const int32_t* offsets, const moe_int8_ffn& w, int y_dtype, void* y, void* ws,
                       const WsLayout& L, hipStream_t st, const moe_debug* dbg, int ksplit, bool clear_flags,
                       int max_rows) {
-  const GemmPlan gp = choose_gemm_plan_i8(s);
+  const GemmPlan gp = choose_gemm_plan_i8(s, L.stream);
   const int E = s.num_experts, H = s.hidden, I = s.intermediate;
   const int slots = s.num_tokens * s.top_k;
   MTile* sb = at<MTile>(ws, L.sched_big);
@@ -670,7 +688,7 @@ moe_status run_ffn_i8(const moe_shape& s, const void* xq, const int32_t* a_rows,
   void* hq = at<void>(ws, L.hq);
   float* hsc = at<float>(ws, L.hsc);
   if (L.stream) {
-    const int tiles = stream_tiles(s, L.max_tiles_small);
+    const int tiles = (int)stream_tiles(s);
     MOE_HIP(stage_mark(dbg, MOE_STAGE_GATE_UP, true, st));
     MOE_HIP(launch_stream_gateup_i8(xq, a_rows, xsc, w, I, H, h, offsets, E, tiles, max_rows, 0, flags, clear_flags,
                                     st));
@@ -770,10 +788,10 @@ GemmI8Plan plan_gemm_i8(int rows, int n, int k, int E) {
   p.s.top_k = 1;
   p.s.num_groups = 1;
   p.s.act_dtype = MOE_BF16;
-  p.gp = choose_gemm_plan_i8(p.s);
+  p.stream = rows > 0 && stream_i8(p.s, (long long)n * k, k);
+  p.gp = choose_gemm_plan_i8(p.s, p.stream);
   tile_bounds(p.s, p.gp, p.max_big, p.max_small);
   if (p.gp.has_big()) p.max_big += kUnits;  // (cut tiles)
-  p.stream = stream_i8(p.gp, p.s, p.max_small, (long long)n * k);
   p.ksplit = p.stream ? 1 : down_parts(p.s, p.gp, p.max_small, true);
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -1481,7 +1499,7 @@ moe_status moe_grouped_gemm_int8(int32_t rows, int32_t n, int32_t k, int32_t num
     // (an fp16 y adds to the flag word, which then has to be clear before)
     if (y_dtype == MOE_F16) MOE_HIP(launch_clear_flags(flags, st));
     MOE_HIP(launch_stream_i8(a, a_scales, b, b_scales, n, k, y_dtype, y, expert_offsets, num_experts,
-                             stream_tiles(p.s, p.max_small), rows, rows, flags, y_dtype != MOE_F16, st));
+                             (int)stream_tiles(p.s), rows, rows, flags, y_dtype != MOE_F16, st));
     return MOE_OK;
   }
   if (!expert_offsets) {

@@ -44,9 +44,12 @@ def within(got, want, slack, dt):
 
 PRODUCTS = [
     # rows per expert, N, K, rows behind the last group
-    ([20, 40], 28672, 8192, 2),                         # 32-row tiles, two parts
+    ([20, 40], 28672, 8192, 2),                         # few rows on large tiles
+    ([10, 15, 0, 3], 16384, 4096, 2),                   # 32-row tiles, two parts
+    ([10, 15, 0, 3], 28688, 4096, 2),                   # 32-row tiles, enough of them: no parts
+    ([3] * 50 + [7] * 14, 2048, 256, 1),                # many experts of few rows
     ([1, 0, 1, 2, 0, 0, 1, 0], 4096, 14336, 0),         # fewer rows than experts: eight parts
-    ([25] * 6 + [50, 0], 16384, 4096, 3),               # 32-row tiles, enough of them: no parts
+    ([25] * 6 + [50, 0], 16384, 4096, 3),               # 16 to 64 rows an expert
     ([33, 0, 1, 30, 16, 17, 32, 31], 12304, 4224, 0),   # the same, ragged
     ([300], 4096, 14336, 1),                            # large tiles, three parts
     ([129, 64, 65, 255, 256, 1, 0, 3], 2064, 8192, 5),  # large tiles of every height, two parts
@@ -100,8 +103,11 @@ FFNS = [
     # H, I, rows per expert, top_k, rows left over
     (7168, 2048, [1] * 8, 8, 0),                        # one token: split gate/up of 32-row tiles, two-part down
     (4096, 14336, [1, 0, 3, 0, 2, 0, 0, 0], 1, 1),      # a few tokens: eight-part down
-    (4096, 14336, [14, 20, 9, 33, 0, 31, 1, 20], 2, 0),  # 32-row tiles, two parts in the down projection
-    (2048, 4224, [60, 1, 33, 64, 32, 0, 90, 50], 2, 4),  # the same, no parts
+    (4096, 14336, [14, 20, 9, 33, 0, 31, 1, 20], 2, 0),  # 16 to 64 rows an expert
+    (2048, 4224, [60, 1, 33, 64, 32, 0, 90, 50], 2, 4),
+    (4096, 14336, [14, 20, 9, 3, 0, 11, 1, 6], 2, 0),    # 32-row tiles, two parts in the down projection
+    (7168, 640, [15, 33, 1, 0, 20, 40, 9, 17, 30, 5, 6, 12, 18, 11, 16, 7], 2, 6),  # the same, no parts
+    (512, 2048, [4, 1, 7, 0] * 16, 4, 8),                # many experts of few rows
     (2048, 14336, [300, 129, 63, 20, 0, 0, 0, 0], 2, 0),  # large tiles, three parts
 ]
 
@@ -161,6 +167,8 @@ BLOCKS = {
     "shared_large": tiny(tokens=40, top_k=2, k_choices=None, capacity_factor=0.0, shared_inter=16384).replace(hidden=2048),
     "large_split": tiny(tokens=150, top_k=2, k_choices=None, capacity_factor=0.0, shared_inter=256).replace(
         hidden=1024, inter=14336, experts=4),
+    "lds_few": tiny(tokens=20, top_k=2, k_choices=None, capacity_factor=0.0).replace(
+        hidden=2048, inter=14336, experts=4),
     "lds_split": tiny(tokens=40, top_k=2, k_choices=None, capacity_factor=0.0).replace(
         hidden=2048, inter=14336, experts=4),
 }
