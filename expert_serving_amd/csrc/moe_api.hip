@@ -229,11 +229,12 @@ GemmPlan choose_gemm_plan(const moe_shape& s) {
 // expert's weights once where it has 16 rows and more on average (one expert of
 // all rows: 64, so that the call without offsets is planned alike), and few rows of
 // many experts fill the compute units without the splits of K that 32-row tiles
-// of few experts have.  FFNs on 32-row tiles against tiles of up to 256: 16
-// rows each, 8 experts of 4096 x 14336, 274 against 262 us, 40
-// rows 356 against 295; 12 rows 230 against 257; 64 experts of 2048 x 1408, 6
-// rows 120 against 112, 60 rows 192 against 133; 256 of 7168 x 2048, 3 rows 1684
-// against 1714, 60 rows 3382 against 2177.
+// of few experts have.  FFNs on 32-row tiles against tiles of up to 256, the rows
+// spread unevenly over the experts: 8 experts of 4096 x 14336, 12 rows each, 230
+// against 257 us, 16 rows 274 against 262 (exactly 16 each: 247 against 269), 40
+// rows 356 against 295; 64 experts of 2048 x 1408, 6 rows 120 against 112, 60 rows
+// 192 against 133; 256 of 7168 x 2048, 3 rows 1684 against 1714, 60 rows 3382
+// against 2177.
 GemmPlan choose_gemm_plan_i8(const moe_shape& s, bool stream) {
   const long long avg = (long long)s.num_tokens * s.top_k / s.num_experts;
   GemmPlan p;
@@ -370,16 +371,19 @@ bool stream_i8(const moe_shape& s, long long matrix_bytes, long long mean_k) {
 // of an FFN whose gate, up and down matrices a tile reads
 bool stream_ffn_i8(const moe_shape& s, long long H, long long I) { return stream_i8(s, 3 * H * I, (2 * H + I) / 3); }
 
-// int8 products whose 256 x 256 tiles (about half an expert's worth more than
-// the rows fill) would leave half the compute units idle run on 128 x 128 ones.
-// Measured, 256 against 128: 1024 rows x 4096 x 4096 (80 tiles) 51 against 32 us,
-// the down projection of 3738 rows over 14 experts, 640 x 4864 (63), 59 against
-// 36; 2000 rows x 4096 x 4096 (128) 57 against 54, 3000 rows (192) 63 against 84,
-// 3000 rows over 16 experts, 2048 x 2048 (152), 35 against 38.  The gate/up
-// product of as few tiles is slower on halves (5364 rows, 768 x 768: 22 against 27).
+// int8 products whose 256 x 256 tiles (half a tile per expert more than the rows
+// fill, and one at least for each expert that has rows) would leave half the
+// compute units idle run on 128 x 128 ones.  Measured, 256 against 128: 1024 rows x
+// 4096 x 4096 (80 tiles) 51 against 32 us, the down projection of 3738 rows over 14
+// experts, 640 x 4864 (63), 59 against 36; 2000 rows x 4096 x 4096 (128) 57 against
+// 54, 3000 rows (192) 63 against 84, 3000 rows over 16 experts, 2048 x 2048 (152),
+// 35 against 38, 120 rows over 2 experts, 28672 x 8192 (224), 101 against 155.  The
+// gate/up product of as few tiles is slower on halves (5364 rows, 768 x 768: 22
+// against 27).
 bool few_tiles_i8(const moe_shape& s, int n) {
-  const long long slots = (long long)s.num_tokens * s.top_k;
-  return (slots / 256 + (s.num_experts + 1) / 2) * ((n + 255) / 256) < kComputeUnits / 2;
+  const long long slots = (long long)s.num_tokens * s.top_k, E = s.num_experts;
+  const long long tiles = std::max(slots / 256 + (E + 1) / 2, std::min(slots, E));
+  return tiles * ((n + 255) / 256) < kComputeUnits / 2;
 }
 
 // The second product of a batch of few and short rows quantises them itself:
