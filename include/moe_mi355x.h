@@ -458,7 +458,10 @@ moe_status moe_quantize_int8(int32_t rows, int32_t cols, int32_t src_dtype, cons
  * moe_dispatch writes them, expert_offsets[num_experts] <= rows; NULL with
  * num_experts == 1 for all rows.  Rows at or beyond
  * expert_offsets[num_experts] are neither read nor written.  An fp16 y out of
- * range sets MOE_FLAG_Y_RANGE in the workspace flag word (and is infinite). */
+ * range sets MOE_FLAG_Y_RANGE in the workspace flag word (and is infinite).
+ * Fewer rows can need the larger workspace (a split of k over partial sums):
+ * a caller of several sizes takes the largest of their workspaces, here as for
+ * the calls with a shape. */
 moe_status moe_workspace_size_gemm_int8(int32_t rows, int32_t n, int32_t k, int32_t num_experts, size_t* bytes);
 moe_status moe_grouped_gemm_int8(int32_t rows, int32_t n, int32_t k, int32_t num_experts, const int8_t* a,
                                  const float* a_scales, const int32_t* expert_offsets, const int8_t* b,
