@@ -14,6 +14,7 @@
 // 4.9 TB/s); 64 rows of 4096 in 4.9 us, of which the launch takes 4.7.
 #include "moe_internal.h"
 #include "quant_int8.h"
+#include "swiglu.h"
 
 namespace moe {
 namespace {
@@ -110,16 +111,17 @@ __device__ __forceinline__ int grid_row() {
   return r < 0x7FFFFFFFu ? (int)r : 0x7FFFFFFF;
 }
 
-// Sum and maximum over the block, in a fixed order, on every thread.
+// Sum, in a fixed order, and maximum over the block, on every thread.
 template <int NT>
-__device__ __forceinline__ void block_sum_max(float& sum, float& top) {
+__device__ __forceinline__ void block_sum_max(float& sum, uint32_t& top) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) {
     sum += __shfl_xor(sum, off, 64);
-    top = fmaxf(top, __shfl_xor(top, off, 64));
+    top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
   }
   if constexpr (NT > 64) {
-    __shared__ float s_sum[NT / 64], s_top[NT / 64];
+    __shared__ float s_sum[NT / 64];
+    __shared__ uint32_t s_top[NT / 64];
     if ((threadIdx.x & 63) == 0) {
       s_sum[threadIdx.x >> 6] = sum;
       s_top[threadIdx.x >> 6] = top;
@@ -130,7 +132,7 @@ __device__ __forceinline__ void block_sum_max(float& sum, float& top) {
 #pragma unroll
     for (int w = 1; w < NT / 64; ++w) {
       sum += s_sum[w];
-      top = fmaxf(top, s_top[w]);
+      top = max(top, s_top[w]);
     }
   }
 }
@@ -138,7 +140,8 @@ __device__ __forceinline__ void block_sum_max(float& sum, float& top) {
 // Norm of a row and / or its int8 codes.  With t = x * weight (the norm's
 // factor 1 / sqrt(mean x^2 + eps) is common to the row and cancels in the
 // codes), one reduction gives both the sum of squares and the row's maximum.
-// NORM false: quantisation of x itself.
+// NORM false: quantisation of x itself.  The maximum is taken over the magnitudes
+// as words, which keeps a NaN.
 template <int DT, int V, int NT, bool NORM>
 __global__ __launch_bounds__(NT) void k_rows(int rows, int cols, const void* x, const float* __restrict__ weight, float eps,
                                              int out_bf16, void* out, uint8_t* __restrict__ codes,
@@ -150,7 +153,8 @@ __global__ __launch_bounds__(NT) void k_rows(int rows, int cols, const void* x, 
   const int granules = cols / G;
   const size_t base = (size_t)r * cols;
   float t[V > 0 ? V : 1][G];
-  float sum = 0.f, top = 0.f;
+  float sum = 0.f;
+  uint32_t top = 0u;
   bool range = false;
   auto take = [&](int g, float* f) {  // t of granule g, its squares and maximum
     load_granule<DT>(x, base + (size_t)g * G, f);
@@ -158,8 +162,8 @@ __global__ __launch_bounds__(NT) void k_rows(int rows, int cols, const void* x, 
       if (h_flags) {
 #pragma unroll
         for (int q = 0; q < G; ++q) {
-          if (fabsf(f[q]) > 65504.f) range = true;
-          f[q] = fminf(fmaxf(f[q], -65504.f), 65504.f);
+          if (!(fabsf(f[q]) <= 65504.f)) range = true;
+          f[q] = clamp_half(f[q]);
         }
       }
     }
@@ -173,7 +177,7 @@ __global__ __launch_bounds__(NT) void k_rows(int rows, int cols, const void* x, 
       }
     }
 #pragma unroll
-    for (int q = 0; q < G; ++q) top = fmaxf(top, fabsf(f[q]));
+    for (int q = 0; q < G; ++q) top = max(top, i8_magnitude(f[q]));
   };
   if constexpr (V > 0) {
 #pragma unroll
@@ -186,7 +190,8 @@ __global__ __launch_bounds__(NT) void k_rows(int rows, int cols, const void* x, 
   }
   block_sum_max<NT>(sum, top);
   const float rstd = NORM ? 1.0f / sqrtf(sum / (float)cols + eps) : 1.0f;
-  const I8Row q8 = i8_row(top);
+  const float amax = __uint_as_float(top);
+  const I8Row q8 = i8_row(amax);
   auto put = [&](int g, const float* f) {
     const size_t i = base + (size_t)g * G;
     if (NORM && out) {
@@ -213,14 +218,12 @@ __global__ __launch_bounds__(NT) void k_rows(int rows, int cols, const void* x, 
     }
   } else {
     for (int g = threadIdx.x; g < granules; g += NT) {
-      float s0 = sum, m0 = top;  // take() adds to them again: unused from here on
-      take(g, t[0]);
-      sum = s0, top = m0;
+      take(g, t[0]);  // (adds to sum and top again: not used from here on)
       put(g, t[0]);
     }
   }
   if (DT == MOE_F16 && range) atomicOr(h_flags, (uint32_t)MOE_FLAG_H_RANGE);
-  if (scales && threadIdx.x == 0) scales[r] = NORM ? top * rstd / 127.0f : top / 127.0f;
+  if (scales && threadIdx.x == 0) scales[r] = NORM ? amax * rstd / 127.0f : amax / 127.0f;
 }
 
 template <int DT, bool NORM>
@@ -345,7 +348,7 @@ __global__ __launch_bounds__(NT) void k_combine_norm(const void* __restrict__ y,
   }
   float rstd = 1.0f;
   if (e.weight) {
-    float none = 0.f;
+    uint32_t none = 0u;
     block_sum_max<NT>(sum, none);
     rstd = 1.0f / sqrtf(sum / (float)H + e.eps);
   }

@@ -911,7 +911,7 @@ __device__ __forceinline__ void gemm_tile(
                 v = silu_mul_exact(v, (float)acc1[DUAL ? a : 0][DUAL ? b : 0][4 * qi + q] * (s[b] * w1[DUAL ? a : 0][qi][q]));
               if (ydt == MOE_F16) {
                 overflow |= real && in && !(fabsf(v) <= 65504.f);
-                if constexpr (DUAL) v = fminf(fmaxf(v, -65504.f), 65504.f);
+                if constexpr (DUAL) v = clamp_half(v);
                 w[q] = f32_to_f16_bits(v);
               } else {
                 w[q] = f32_to_bf16_rne(v);

@@ -63,8 +63,7 @@ __global__ __launch_bounds__(256) void k_swiglu_parts_i8(const int32_t* __restri
     for (int q = 0; q < 4; ++q) {
       float v = silu_mul_exact((float)gs[q] * (s * g4[q]), (float)us[q] * (s * u4[q]));
       overflow |= !(fabsf(v) <= 65504.f);
-      v = fminf(fmaxf(v, -65504.f), 65504.f);
-      w[q] = f32_to_f16_bits(v);
+      w[q] = f32_to_f16_bits(clamp_half(v));
     }
     *reinterpret_cast<uint2*>(h + (size_t)row * N + c) = uint2{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
   }

@@ -6,6 +6,12 @@
 
 namespace moe {
 
+// |v| as a word.  The largest of a row's words is that of its largest magnitude,
+// or of a NaN where the row holds one (a NaN's is above infinity's), so that a row
+// that is not finite gets a scale that is not: products of its unspecified codes
+// are then no plausible numbers.
+__device__ __forceinline__ uint32_t i8_magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
 // What a row of maximum magnitude amax needs for its codes 127 v / amax.
 struct I8Row {
   float pre;   // power of two that keeps 127 v and 1 / amax inside fp32's normal range

@@ -118,8 +118,8 @@ __device__ __forceinline__ void codes8(const u32x4 w, const I8Row& r, uint32_t& 
   for (int q = 0; q < 4; ++q) {
     const uint32_t x = w[q];
     const f16x2 h = __builtin_bit_cast(f16x2, x);
-    c[2 * q] = i8_code(fminf(fmaxf((float)h[0], -65504.f), 65504.f), r);
-    c[2 * q + 1] = i8_code(fminf(fmaxf((float)h[1], -65504.f), 65504.f), r);
+    c[2 * q] = i8_code(clamp_half((float)h[0]), r);
+    c[2 * q + 1] = i8_code(clamp_half((float)h[1]), r);
   }
   lo = i8_pack4(c[0], c[1], c[2], c[3]);
   hi = i8_pack4(c[4], c[5], c[6], c[7]);
@@ -164,10 +164,10 @@ __device__ __forceinline__ void stream_tile(int32_t* __restrict__ smem, const St
 
   // QUANT: the row's maximum, over this wavefront's steps, the four lanes of a
   // row, and the wavefronts
-  __shared__ float s_top[QUANT ? kWaves : 1][16];
+  __shared__ uint32_t s_top[QUANT ? kWaves : 1][16];
   I8Row q8{};
   if constexpr (QUANT) {
-    float top = 0.f;
+    uint32_t top = 0u;
     for (int s = 0; s < mine; ++s)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {  // two operands of 16 values
@@ -177,17 +177,18 @@ __device__ __forceinline__ void stream_tile(int32_t* __restrict__ smem, const St
         for (int i = 0; i < 4; ++i) {
           const uint32_t x = w[i];
           const f16x2 h = __builtin_bit_cast(f16x2, x);
-          top = fmaxf(top, fmaxf(fabsf((float)h[0]), fabsf((float)h[1])));
+          top = max(top, max(i8_magnitude((float)h[0]), i8_magnitude((float)h[1])));
         }
       }
-    top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
     if (lane < 16) s_top[wave][lane] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_top[w][lr]);
-    if (top > 65504.f && n0 == 0 && a.flags) atomicOr(a.flags, (uint32_t)MOE_FLAG_H_RANGE);
-    q8 = i8_row(fminf(top, 65504.f));
+    for (int w = 0; w < kWaves; ++w) top = max(top, s_top[w][lr]);
+    const float amax = __uint_as_float(top);
+    if (!(amax <= 65504.f) && n0 == 0 && a.flags) atomicOr(a.flags, (uint32_t)MOE_FLAG_H_RANGE);
+    q8 = i8_row(clamp_half(amax));
   }
 
   u32x4 wv[D][NB][F][2], av[D][MH][2];
@@ -273,7 +274,7 @@ __device__ __forceinline__ void stream_tile(int32_t* __restrict__ smem, const St
   bool overflow = false;
   if constexpr (DUAL) {
     // (a value out of fp16's range becomes infinite: the quantisation of the
-    // row takes it back to the largest one and sets the flag)
+    // row takes it back to the largest one and sets the flag, as for a NaN, which stays)
     const f32x4 b1 = *reinterpret_cast<const f32x4*>(a.sb1 + (size_t)t.expert * N + n);
     const float s = a.sa[a.a_rows ? a.a_rows[row] : row];
     uint32_t w[4];
@@ -284,10 +285,10 @@ __device__ __forceinline__ void stream_tile(int32_t* __restrict__ smem, const St
   } else {
     float s;
     if constexpr (QUANT) {
-      s = 0.f;
+      uint32_t top = 0u;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) s = fmaxf(s, s_top[w][r]);
-      s = fminf(s, 65504.f) / 127.0f;
+      for (int w = 0; w < kWaves; ++w) top = max(top, s_top[w][r]);
+      s = clamp_half(__uint_as_float(top)) / 127.0f;
     } else {
       s = a.sa[row];
     }

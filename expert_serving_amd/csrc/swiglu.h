@@ -5,6 +5,13 @@
 
 namespace moe {
 
+// v with values outside fp16's range taken as the largest in it; a NaN stays
+// one (the minimum and maximum alone would make a number of it).
+__device__ __forceinline__ float clamp_half(float v) {
+  const float c = fminf(fmaxf(v, -65504.f), 65504.f);
+  return v == v ? c : v;
+}
+
 // silu(g) = g / (1 + e^-g).  The rounding of -g * log2 e is carried into the
 // exponential (without it the result is off by |g| roundings, with it by one
 // or two), and the reciprocal is the hardware's, about one rounding.

@@ -70,7 +70,7 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 #define MOE_FLAG_BAD_K 1u       /* some k_per_token[t] outside [1, top_k]: token routed nowhere */
 #define MOE_FLAG_BAD_EXPERT 2u  /* some topk_ids entry outside [-1, E): slot treated as unused  */
 #define MOE_FLAG_H_RANGE 4u     /* some SwiGLU activation h exceeded fp16 range (bf16 and int8
-                                   experts) or was not finite (MXFP8 experts)                 */
+                                   experts) or was not finite (MXFP8 experts; int8: or NaN)   */
 #define MOE_FLAG_BAD_REPLICA 8u /* a routed expert without a replica, or a replica id out of range */
 #define MOE_FLAG_Y_RANGE 16u    /* some expert output exceeded fp16 range inside a layer call
                                    (moe_layer_forward, moe_layer_forward_mxfp8), a block call or
@@ -446,8 +446,9 @@ moe_status moe_route_biased(const moe_shape* shape, const void* x, const void* w
 
 /* Quantises src [rows][cols] (MOE_BF16, MOE_F32 or MOE_F16; cols a multiple
  * of 128) to codes [rows][cols] and scales [rows].  Weights are quantised once
- * with this call (rows = E*I or E*H).  Inputs are assumed finite (a row with an
- * infinity or NaN gets unspecified codes). */
+ * with this call (rows = E*I or E*H).  A row with an infinity or NaN gets
+ * unspecified codes and a scale that is infinite or NaN (NaN for a NaN), so that
+ * products of it are not finite either. */
 moe_status moe_quantize_int8(int32_t rows, int32_t cols, int32_t src_dtype, const void* src, int8_t* codes,
                              float* scales, void* stream);
 
@@ -484,9 +485,10 @@ moe_status moe_workspace_size_int8(const moe_shape* shape, size_t* bytes);
 /* S7-S8 with int8 operands: as moe_grouped_ffn, with x_perm given as codes
  * [T*top_k][H] and scales [T*top_k]; h = silu(a) * u (fp32) is rounded to fp16
  * -- values outside its range are clamped to it and set MOE_FLAG_H_RANGE -- and
- * quantised per row before the down projection; y_perm in y_dtype (MOE_F32, or
- * MOE_F16 or MOE_BF16; an fp16 value out of range sets MOE_FLAG_Y_RANGE).
- * Clears the workspace flag word. */
+ * quantised per row before the down projection; a NaN in a row of h, as a NaN
+ * scale leaves it, sets the flag and makes the y row NaN.  y_perm in y_dtype
+ * (MOE_F32, or MOE_F16 or MOE_BF16; an fp16 value out of range sets
+ * MOE_FLAG_Y_RANGE).  Clears the workspace flag word. */
 moe_status moe_grouped_ffn_int8(const moe_shape* shape, const int8_t* x_codes, const float* x_scales,
                                 const int32_t* expert_offsets, const moe_int8_ffn* experts, int32_t y_dtype,
                                 void* y_perm, void* ws, size_t ws_bytes, void* stream);
@@ -517,8 +519,9 @@ typedef struct {
  * n = norm(x) of rows [rows][cols] (src_dtype MOE_F32 or MOE_BF16; cols a
  * multiple of 64, of 4 when src and out are fp32, of 128 with codes); out
  * (nullable) in out_dtype (MOE_F32 or MOE_BF16); codes and scales (both or
- * neither) quantise the unrounded n as moe_quantize_int8 does.  weight [cols]
- * fp32 or NULL (1).  out may be x itself when the types are the same. */
+ * neither) quantise the unrounded n as moe_quantize_int8 does (a row of x with
+ * an infinity or NaN gets the scale NaN).  weight [cols] fp32 or NULL (1).  out
+ * may be x itself when the types are the same. */
 moe_status moe_norm(int32_t rows, int32_t cols, int32_t src_dtype, const void* x, const float* weight, float eps,
                     int32_t out_dtype, void* out, int8_t* codes, float* scales, void* stream);
 
