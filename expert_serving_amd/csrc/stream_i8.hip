@@ -273,14 +273,17 @@ __device__ __forceinline__ void stream_tile(int32_t* __restrict__ smem, const St
   const f32x4 b0 = *reinterpret_cast<const f32x4*>(a.sb0 + (size_t)t.expert * N + n);
   bool overflow = false;
   if constexpr (DUAL) {
-    // (a value out of fp16's range becomes infinite: the quantisation of the
-    // row takes it back to the largest one and sets the flag, as for a NaN, which stays)
+    // A value out of fp16's range, also one that would round to the largest in it,
+    // becomes infinite (a NaN stays): the quantisation of the row takes it back to
+    // the largest one and sets the flag, which this launch may be clearing.
     const f32x4 b1 = *reinterpret_cast<const f32x4*>(a.sb1 + (size_t)t.expert * N + n);
     const float s = a.sa[a.a_rows ? a.a_rows[row] : row];
     uint32_t w[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      w[q] = f16_bits(silu_mul_exact((float)sum[0][q] * (s * b0[q]), (float)sum[NB - 1][q] * (s * b1[q])));
+    for (int q = 0; q < 4; ++q) {
+      const float v = silu_mul_exact((float)sum[0][q] * (s * b0[q]), (float)sum[NB - 1][q] * (s * b1[q]));
+      w[q] = f16_bits(fabsf(v) <= 65504.f ? v : v * __builtin_inff());
+    }
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) = uint2{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
   } else {
     float s;

@@ -1,11 +1,12 @@
-"""NaN and infinities in the int8 operators, on every plan of the products: what is not a number stays visible as one,
-and the same values set the same flags whatever the batch."""
+"""NaN, infinities and values just outside fp16's range in the int8 operators, on every plan of the products: what is
+not a number stays visible as one, and the same values set the same flags whatever the batch."""
 
 import pytest
 import torch
 
 from expert_serving_amd import abi
 
+import plain_block as P
 from gpu_util import dev, f32, say
 from test_gpu_block import Block, tiny
 from test_gpu_int8 import DT, offsets_of, on, run_ffn
@@ -126,3 +127,33 @@ def test_a_nan_token_of_the_int8_block(tokens, norms):
     keep = [t for t in range(tokens) if t != tokens // 2]
     assert torch.isnan(out[tokens // 2]).all() and torch.equal(out[keep], want[keep])
     assert f0 == 0 and f1 & H_RANGE
+
+
+def line(name, gate, up):
+    """Every h is silu(gate) * up in row 0, and of 2^-8 times smaller gates and ups in the others: row codes 1, weight
+    codes 1 in the first column and 0 elsewhere, so that the int32 sums are 1."""
+    H, I, E, off, k = plan(name)
+    rows = int(off[-1])
+    x = torch.ones(rows, H, dtype=torch.int8, device=dev())
+    xs = torch.full((rows,), 2.0 ** -8, device=dev())
+    xs[0] = 1.0
+    first = torch.zeros(E, I, H, dtype=torch.int8, device=dev())
+    first[:, :, 0] = 1
+    down = torch.ones(E, H, I, dtype=torch.int8, device=dev())
+    of = lambda v, n: torch.full((E, n), v, device=dev())  # noqa: E731
+    w = abi.int8_ffn((first, of(gate, I)), (first, of(up, I)), (down, of(2.0 ** -16, H)))
+    y, flags = run_ffn(x, xs, on(off), w, H, I, E, rows // k, k, "f32")
+    return y, flags, 127.0 * I * 2.0 ** -16 / 127   # y of a row of equal h is h times the last
+
+
+@pytest.mark.parametrize("name", PLANS)
+def test_h_between_the_largest_fp16_value_and_its_rounding(name):
+    """fp32 values above 65504 that round to it are out of range on every plan; 65504 itself is not.  silu(256) is 256,
+    so h is one rounding of 256 times the up value (exact for these), y four more of fp32 and up to eight parts."""
+    for up, flag in ((255.875, 0), (65510.0 / 256, H_RANGE), (65519.0 / 256, H_RANGE), (65520.0 / 256, H_RANGE),
+                     (1024.0, H_RANGE)):
+        for sign in (1.0, -1.0):
+            y, flags, f = line(name, 256.0, sign * up)
+            assert flags == flag, (up, sign)
+            want = sign * 65504.0 * f
+            assert torch.all((y[0] - want).abs() <= 12 * P.U32 * abs(want)), (up, sign)
