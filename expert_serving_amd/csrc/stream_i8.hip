@@ -36,6 +36,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8;
 constexpr int kStep = 128;  // codes of a step
@@ -111,15 +112,15 @@ __device__ __forceinline__ Tile find_tile(const StreamArgs& a, int index, int la
 }
 
 // Four fp16 words (8 values) to 8 codes, with values out of range taken as the
-// largest in it.
+// largest in it (a row with a NaN has the scale NaN, whatever its codes).
 __device__ __forceinline__ void codes8(const u32x4 w, const I8Row& r, uint32_t& lo, uint32_t& hi) {
   int c[8];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const uint32_t x = w[q];
     const f16x2 h = __builtin_bit_cast(f16x2, x);
-    c[2 * q] = i8_code(clamp_half((float)h[0]), r);
-    c[2 * q + 1] = i8_code(clamp_half((float)h[1]), r);
+    c[2 * q] = i8_code(fminf(fmaxf((float)h[0], -65504.f), 65504.f), r);
+    c[2 * q + 1] = i8_code(fminf(fmaxf((float)h[1], -65504.f), 65504.f), r);
   }
   lo = i8_pack4(c[0], c[1], c[2], c[3]);
   hi = i8_pack4(c[4], c[5], c[6], c[7]);
@@ -167,19 +168,18 @@ __device__ __forceinline__ void stream_tile(int32_t* __restrict__ smem, const St
   __shared__ uint32_t s_top[QUANT ? kWaves : 1][16];
   I8Row q8{};
   if constexpr (QUANT) {
-    uint32_t top = 0u;
+    u16x2 tops = {0, 0};  // magnitudes of halves order as words do
     for (int s = 0; s < mine; ++s)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {  // two operands of 16 values
         const u32x4 w = *reinterpret_cast<const u32x4*>(ap[0] + ((size_t)s * (kWaves * kStep) + 64 * (q >> 1)) * 2 +
                                                         16 * (q & 1));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t x = w[i];
-          const f16x2 h = __builtin_bit_cast(f16x2, x);
-          top = max(top, max(i8_magnitude((float)h[0]), i8_magnitude((float)h[1])));
-        }
+        for (int i = 0; i < 4; ++i)
+          tops = __builtin_elementwise_max(tops, __builtin_bit_cast(u16x2, (uint32_t)(w[i] & 0x7FFF7FFFu)));
       }
+    const uint16_t half = tops[0] > tops[1] ? tops[0] : tops[1];
+    uint32_t top = i8_magnitude((float)__builtin_bit_cast(_Float16, half));
     top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
     top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
     if (lane < 16) s_top[wave][lane] = top;
