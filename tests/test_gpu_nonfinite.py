@@ -157,3 +157,13 @@ def test_h_between_the_largest_fp16_value_and_its_rounding(name):
             assert flags == flag, (up, sign)
             want = sign * 65504.0 * f
             assert torch.all((y[0] - want).abs() <= 12 * P.U32 * abs(want)), (up, sign)
+
+
+@pytest.mark.parametrize("name", PLANS)
+def test_h_of_gates_near_the_largest_float(name):
+    """silu of a huge gate is the gate, and of a huge negative one zero: clamped and flagged, not a NaN."""
+    for gate, up, h, flag in ((3.0e38, 1.0, 65504.0, H_RANGE), (3.0e38, -1.0, -65504.0, H_RANGE),
+                              (-3.0e38, 1.0, 0.0, 0), (1.0e38, 1.0, 65504.0, H_RANGE)):
+        y, flags, f = line(name, gate, up)
+        assert flags == flag, (gate, up)
+        assert torch.all((y[0] - h * f).abs() <= 12 * P.U32 * abs(h) * f), (gate, up)
