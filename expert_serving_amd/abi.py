@@ -76,6 +76,7 @@ class MoeBlock(ctypes.Structure):
                 ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float), ("gate", ctypes.c_void_p),
                 ("gate_row_stride", ctypes.c_int64), ("gate_col_stride", ctypes.c_int32),
                 ("gate_dtype", ctypes.c_int32), ("stream_dtype", ctypes.c_int32)]
+    gate_tensor = None  # (pointer, rows, columns) of the gate that make_block was given
 
 
 class MoeError(RuntimeError):
@@ -446,7 +447,8 @@ def moe_norm(rows, cols, src_dtype, x, weight, eps, out_dtype, out, codes, scale
 def make_block(select_bias=None, pre_norm=None, post_norm=None, eps=1e-6, gate=None, residual_scale=1.0,
                stream_dtype=MOE_BF16) -> MoeBlock:
     """A moe_block from device tensors.  gate: a bf16 or fp32 tensor that broadcasts to [T, H] -- [H] or [1, H]
-    (a value per channel), [T, 1] (a value per token) or [T, H], rows at any stride, columns one apart."""
+    (a value per channel), [T, 1] (a value per token) or [T, H], rows at any stride, columns one apart; of more
+    rows than the call has tokens the first are taken, any other size is refused by the call."""
     b = MoeBlock(_ptr(select_bias), _ptr(pre_norm), _ptr(post_norm), float(eps), float(residual_scale), _ptr(gate),
                  0, 0, MOE_F32, int(stream_dtype))
     if gate is not None:
@@ -459,11 +461,22 @@ def make_block(select_bias=None, pre_norm=None, post_norm=None, eps=1e-6, gate=N
         b.gate_row_stride = gate.stride(0) if rows > 1 else 0
         b.gate_col_stride = gate.stride(-1) if cols > 1 else 0
         b.gate_dtype = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}[gate.dtype]
+        b.gate_tensor = (gate.data_ptr(), rows, cols)
     b.tensors = (select_bias, pre_norm, post_norm, gate)
     return b
 
 
+def _check_gate(shape, block):
+    """The gate's rows and columns, which the strides in the struct do not show, against the call's."""
+    if block.gate_tensor is None or block.gate_tensor[0] != (block.gate or 0):
+        return
+    _, rows, cols = block.gate_tensor
+    if (rows != 1 and rows < shape.num_tokens) or cols not in (1, shape.hidden):
+        raise ValueError(f"a gate of {rows} x {cols} for {shape.num_tokens} tokens of {shape.hidden} channels")
+
+
 def moe_combine_norm(shape, block, y_dtype, y_perm, row_of_slot, topk_gates, y_shared, residual, out, stream=None):
+    _check_gate(shape, block)
     _check(lib().moe_combine_norm(ctypes.byref(shape), ctypes.byref(block), int(y_dtype), _ptr(y_perm),
                                   _ptr(row_of_slot), _ptr(topk_gates), _ptr(y_shared), _ptr(residual), _ptr(out),
                                   _stream(stream)), "moe_combine_norm")
@@ -483,6 +496,7 @@ def _dbg(dbg):
 
 def moe_block_forward(shape, block, x, w_router, router_bias, k_per_token, w_gate, w_up, w_down, ws_gate, ws_up,
                       ws_down, out, dbg, ws, ws_bytes=None, stream=None):
+    _check_gate(shape, block)
     d = _dbg(dbg)
     _check(lib().moe_block_forward(ctypes.byref(shape), ctypes.byref(block), _ptr(x), _ptr(w_router),
                                    _ptr(router_bias), _ptr(k_per_token), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
@@ -494,6 +508,7 @@ def moe_block_forward(shape, block, x, w_router, router_bias, k_per_token, w_gat
 
 def moe_block_forward_int8(shape, block, x, w_router, router_bias, k_per_token, experts, shared, out, dbg, ws,
                            ws_bytes=None, stream=None):
+    _check_gate(shape, block)
     d = _dbg(dbg)
     _check(lib().moe_block_forward_int8(ctypes.byref(shape), ctypes.byref(block), _ptr(x), _ptr(w_router),
                                         _ptr(router_bias), _ptr(k_per_token), _mx(experts), _mx(shared), _ptr(out),

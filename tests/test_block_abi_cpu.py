@@ -218,3 +218,27 @@ def test_strided_tensors_are_not_quantised_on_another_stream():
     import torch
     with pytest.raises(ValueError):
         abi.quantize_int8(torch.zeros(128, 128).t(), stream=1)
+
+
+@pytest.mark.parametrize("dims,tokens,taken", [
+    ((64,), 5, True), ((1, 64), 5, True), ((5, 1), 5, True), ((5, 64), 5, True), ((1, 1), 5, True), ((1,), 5, True),
+    ((9, 64), 5, True), ((9, 1), 5, True), ((5, 1), 0, True), ((0, 64), 0, True),   # rows of a padded batch
+    ((32,), 5, False), ((1, 65), 5, False), ((5, 128), 5, False), ((4, 1), 5, False), ((2, 64), 5, False),
+    ((0, 1), 5, False), ((5, 0), 5, False), ((64, 5), 5, False),
+])
+def test_gates_that_do_not_fit_the_call_are_refused(dims, tokens, taken):
+    """Before the library sees them: their strides would be walked past the end of the tensor.  (What fits reaches the
+    library, which finds that the other arguments are missing.)"""
+    import torch
+    s = abi.make_shape(num_tokens=tokens, hidden=64, num_experts=4, intermediate=64)
+    b = abi.make_block(gate=torch.zeros(dims))
+    calls = (lambda: abi.moe_combine_norm(s, b, F16, None, None, None, None, None, None, stream=1),
+             lambda: abi.moe_block_forward(s, b, *[None] * 11, None, None, 0, stream=1),
+             lambda: abi.moe_block_forward_int8(s, b, *[None] * 7, None, None, 0, stream=1))
+    for f in calls:
+        with pytest.raises(abi.MoeError if taken else ValueError):
+            f()
+    if 0 not in dims:
+        b.gate, b.gate_row_stride = None, 0                  # (the struct is the caller's)
+        with pytest.raises(abi.MoeError):
+            calls[0]()
