@@ -252,8 +252,8 @@ __device__ __forceinline__ bool keep_groups(uint32_t (&w)[EPL], const RouteArgs&
   if (a.lpg > 4) merge([](uint32_t v) { return dpp<0x141>(v); });  // eights mirrored
   if (a.lpg > 8) merge([](uint32_t v) { return dpp<0x140>(v); });  // sixteens mirrored
   if constexpr (TEAM == 64) {
+    // (two groups: at most 32 lanes each)
     if (a.lpg > 16) merge([](uint32_t v) { return (uint32_t)__shfl_xor((int)v, 16, 64); });
-    if (a.lpg > 32) merge([](uint32_t v) { return (uint32_t)__shfl_xor((int)v, 32, 64); });
   }
   float total = rank_value(top[0]), size = fabsf(total);
 #pragma unroll

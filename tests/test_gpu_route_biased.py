@@ -232,3 +232,27 @@ def test_a_zero_bias_is_the_plain_router():
     abi.moe_route_topk(s, None, None, None, lg, None, None, a, ga, ws)
     abi.moe_route_biased(s, None, None, None, torch.zeros(128, device=dev()), lg, None, None, b, gb, ws)
     assert torch.equal(a, b) and torch.allclose(ga, gb, rtol=1e-6, atol=0)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,topn", [(2, 1), (16, 1), (16, 2), (72, 1), (72, 2), (72, 3), (256, 1), (256, 2), (256, 3),
+                                    (256, 8), (510, 2), (512, 3)])
+def test_two_groups(E, topn, score):
+    """Half the experts a group: the widest merges of the groups' lists, with keys far apart and closer than fp32."""
+    say(f"route_biased two groups of {E // 2}, topn {topn}, {score}")
+    r = np.random.default_rng(E * 10 + topn)
+    k = min(8, E // 2)
+    o = dict(score=score, G=2, topn=topn)
+    for T in (1, 203):
+        logits, bias = r.normal(size=(T, E)) * 2, r.normal(size=E) * (0.2 if score == "sigmoid" else 0.5 / E)
+        check(logits, bias, k, keep=1, **o)
+        check(logits, bias, k, keep=2, **o)
+        base = r.choice(np.array([-2.0, 0.25, 1.0], np.float32), size=(T, E))
+        near = np.where(r.random((T, E)) < 0.5, np.nextafter(base, np.float32(9)), base)
+        near[:, E // 2:] = near[:, :E // 2]               # equal groups: the lower one
+        near[1::3, E - 1] = np.nextafter(np.float32(1), np.float32(9))
+        check(near, np.zeros(E), k, keep=1, **o)
+        out = np.zeros(E)
+        out[:E // 2 - 1] = NEG                            # one expert left in the first group
+        check(logits, out, k, keep=1, **o)
+        check(logits, out, k, keep=2, **o)
