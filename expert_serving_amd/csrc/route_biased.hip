@@ -3,9 +3,11 @@
 //
 // The choice is discrete, so it has to be that of the fp64 keys: fp32 sigmoids
 // saturate (17 and 18 become the same score) and their last bit differs from
-// one implementation to the next, while two fp64 keys that differ at all
-// differ by far more than fp64 rounding for any logits and biases given in
-// fp32.  fp64 exponentials and compares of every expert would bound the kernel
+// one implementation to the next, while the fp64 keys of different fp32 logits
+// in the range that routers give differ by far more than fp64 rounding.  fp64 has
+// limits of its own -- sigmoids of logits above 36.8 are all 1, and a bias of
+// magnitude m leaves the scores beside it a resolution of m * 1e-16 -- and keys
+// that are equal there go to the lower expert.  fp64 exponentials and compares of every expert would bound the kernel
 // (8192 tokens of 256 experts: 26 us), so a token is first routed
 // on fp32 keys with a bound on their error; where any decision -- the next expert
 // of a slot, the last group kept -- falls within the bound, which random logits

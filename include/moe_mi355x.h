@@ -426,9 +426,11 @@ moe_status moe_layer_forward_mxfp8(const moe_shape* shape, const void* x, const 
  *   an expert get id -1 and gate 0;
  *   gates: s of the selected experts, divided by their sum when renormalize
  *   (for a sum of 0, gates of 0), times routed_scale.
- * Keys, group scores and gates are computed in fp64, so the choice depends on
- * no rounding in practice; gates are rounded once.  select_bias [E] fp32; the
- * other arguments as for moe_route_topk.  Clears the workspace flag word. */
+ * Keys, group scores and gates are computed in fp64; gates are rounded once.
+ * Keys that are equal in fp64 are equal: the sigmoids of all logits above 36.8
+ * are 1, and beside a bias of magnitude m scores less than about m * 1e-16
+ * apart make one key.  select_bias [E] fp32; the other arguments as for
+ * moe_route_topk.  Clears the workspace flag word. */
 moe_status moe_route_biased(const moe_shape* shape, const void* x, const void* w_router,
                             const float* router_bias, const float* select_bias, const float* logits_in,
                             float* logits_out, const int32_t* k_per_token, int32_t* topk_ids,

@@ -256,3 +256,19 @@ def test_two_groups(E, topn, score):
         out[:E // 2 - 1] = NEG                            # one expert left in the first group
         check(logits, out, k, keep=1, **o)
         check(logits, out, k, keep=2, **o)
+
+
+def test_keys_that_are_equal_in_fp64_go_to_the_lower_expert():
+    """Sigmoids of logits from 37 on are 1; scores far below a bias's resolution leave its keys equal."""
+    logits = np.tile(np.arange(30, 46, dtype=np.float32), (3, 1))
+    ids, gates, _ = check(logits, np.zeros(16), 12)
+    assert np.array_equal(ids[0], [7, 8, 9, 10, 11, 12, 13, 14, 15, 6, 5, 4]) and (gates[0, :9] == gates[0, 0]).all()
+    ids, _, _ = check(logits[:, ::-1], np.zeros(16), 4)
+    assert np.array_equal(ids[0], [0, 1, 2, 3])
+    ids, _, _ = check(logits, np.zeros(16), 4, G=4, keep=2, topn=2)      # groups 2 and 3 tie, then their experts
+    assert np.array_equal(ids[0], [8, 9, 10, 11])
+    small = np.array([[-43, -42, -41, -40, 0]] * 2, np.float32)
+    ids, _, _ = check(small, np.zeros(5), 4, score="softmax")
+    assert np.array_equal(ids[0], [4, 3, 2, 1])
+    ids, _, _ = check(small, np.full(5, 100.0), 4, score="softmax")
+    assert np.array_equal(ids[0], [4, 0, 1, 2])
