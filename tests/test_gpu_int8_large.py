@@ -221,3 +221,25 @@ def test_rows_and_outputs_past_32_bit_offsets(offsets):
             assert bool((y[r, :-1] == f * K).all()) and float(y[r, -1]) == -f * K, (rows, r)
         assert flags == 0
         del a, w, y
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,N,K,parts", [(60, 28672, 8192, 2), (64, 4096, 14336, 3), (100, 4096, 14336, 3),
+                                            (300, 4096, 14336, 3), (700, 1040, 14336, 3), (2100, 512, 16384, 4)])
+def test_split_products_of_all_rows(rows, N, K, parts, dt):
+    """Without offsets: K in parts, for each height of the row tiles, and the sum of the parts."""
+    say(f"int8 gemm of all rows {rows} x {N} x {K} {dt}")
+    assert abi.moe_workspace_size_gemm_int8(rows, N, K, 1) >= parts * rows * N * 4
+    g = gen(rows + N)
+    a, sa = codes(g, rows, K), torch.randn(rows, generator=g, device=dev()).exp()
+    w, sw = codes(g, 1, N, K), scales(g, (1, N), K)
+    y, flags = product(a, sa, None, w, sw, dt)
+    f = sa[:, None].double() * sw[0].double()
+    slack = 11 * P.U32 * mm(a.double().abs(), w[0].double().abs()) * f
+    assert within(y, mm(a, w[0]) * f, slack, dt) and flags == 0
+    if dt == "f16":
+        big = sa.clone()
+        big[rows // 2] = 1e9
+        y2, flags = product(a, big, None, w, sw, dt)
+        keep = [r for r in range(rows) if r != rows // 2]
+        assert flags == abi.MOE_FLAG_Y_RANGE and torch.equal(y2[keep], y[keep])
