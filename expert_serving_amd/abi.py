@@ -8,6 +8,7 @@ functions, and a missing library raises instead of falling back.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -302,13 +303,23 @@ def moe_convert_bf16_to_f16(n, src, dst, stream=None):
     _check(lib().moe_convert_bf16_to_f16(int(n), _ptr(src), _ptr(dst), _stream(stream)), "moe_convert_bf16_to_f16")
 
 
+def _tensors_on(stream, device):
+    """Context in which a helper makes the tensors of a call on `stream`: torch hands freed memory out again in the
+    order of the work of the stream it was allocated on, so memory of another stream could still be in use."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device))
+
+
 def to_f16_weights(w, stream=None):
     """fp16 copy (a float16 tensor) of a bf16 device weight tensor, made by the
     library's conversion, for shapes with down_dtype = MOE_F16."""
     import torch
     assert w.dtype == torch.bfloat16
-    out = torch.empty(w.shape, dtype=torch.float16, device=w.device)
-    moe_convert_bf16_to_f16(w.numel(), w.contiguous(), out, stream)
+    with _tensors_on(stream, w.device):
+        out = torch.empty(w.shape, dtype=torch.float16, device=w.device)
+        moe_convert_bf16_to_f16(w.numel(), w.contiguous(), out, stream)
     return out
 
 
@@ -324,10 +335,11 @@ def quantize_mxfp8(t, scale_stride: Optional[int] = None, stream=None):
     K = t.shape[-1]
     rows = t.numel() // K
     stride = rows if scale_stride is None else scale_stride
-    codes = torch.empty(t.shape, dtype=torch.uint8, device=t.device)
-    scales = torch.empty(max(mx_scale_bytes(rows, K, stride), 16), dtype=torch.uint8, device=t.device)
     dt = MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32
-    moe_quantize_mxfp8(rows, K, dt, t.contiguous(), stride, codes, scales, stream)
+    with _tensors_on(stream, t.device):
+        codes = torch.empty(t.shape, dtype=torch.uint8, device=t.device)
+        scales = torch.empty(max(mx_scale_bytes(rows, K, stride), 16), dtype=torch.uint8, device=t.device)
+        moe_quantize_mxfp8(rows, K, dt, t.contiguous(), stride, codes, scales, stream)
     return codes, scales
 
 
@@ -392,14 +404,15 @@ def moe_quantize_int8(rows, cols, src_dtype, src, codes, scales, stream=None):
 
 def quantize_int8(t, stream=None):
     """(codes int8 of t's shape, scales fp32 of its leading dimensions) of a bf16, fp32 or fp16 device tensor
-    (contiguous when a stream is given: a copy of it would be made on torch's current stream)."""
+    (contiguous when a stream is given, on which codes and scales are then allocated)."""
     import torch
     if stream is not None and not t.is_contiguous():
         raise ValueError("a tensor quantised on a given stream has to be contiguous")
     dt = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}[t.dtype]
-    codes = torch.empty(t.shape, dtype=torch.int8, device=t.device)
-    scales = torch.empty(t.shape[:-1], dtype=torch.float32, device=t.device)
-    moe_quantize_int8(scales.numel(), t.shape[-1], dt, t.contiguous(), codes, scales, stream)
+    with _tensors_on(stream, t.device):
+        codes = torch.empty(t.shape, dtype=torch.int8, device=t.device)
+        scales = torch.empty(t.shape[:-1], dtype=torch.float32, device=t.device)
+        moe_quantize_int8(scales.numel(), t.shape[-1], dt, t.contiguous(), codes, scales, stream)
     return codes, scales
 
 

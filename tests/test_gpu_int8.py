@@ -255,3 +255,24 @@ def test_ffn_of_large_gates():
         want, slack = P.ffn_int8(np64(x), np.ones(1), np.array([0, 1]), *((t.cpu().numpy(), sc.cpu().numpy())
                                  for t, sc in (w["gate"], w["up"], w["down"])))
         assert np.all(np.abs(np64(y) - want) <= slack), s
+
+
+def test_helpers_on_a_given_stream_own_their_memory():
+    """Memory freed while the current stream still has work on it is not handed to a call on another stream."""
+    side = torch.cuda.Stream()
+    x = torch.randn(2048, 4096, device=dev()).to(torch.bfloat16)
+    busy = torch.empty(1 << 30, dtype=torch.uint8, device=dev())
+    makers = (lambda st: abi.quantize_int8(x, stream=st), lambda st: abi.quantize_mxfp8(x, stream=st),
+              lambda st: (abi.to_f16_weights(x, stream=st),))
+    for make in makers:
+        want = [t.clone() for t in make(None)]
+        torch.cuda.synchronize()
+        for _ in range(40):                            # some milliseconds of work before the last use
+            busy.fill_(1)
+        late = [torch.empty_like(t) for t in want]
+        for t in late:
+            t.zero_()
+        del late, t
+        got = make(side.cuda_stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
