@@ -8,10 +8,11 @@
 // block takes one row; a thread owns granules of 16 loaded bytes (8 values of 2
 // bytes, 4 of 4), granule g of the row in thread g % NT, V of them per thread.
 // Rows too long for that (V = 0) are read a second time.
-// Measured: norm of 8192 x 7168 fp32 to bf16 and codes 79.7 us (352 MB, 4.4 TB/s,
-// a device copy 4.7), 65536 x 1024 fp16 to codes 39 us; combine of 8192 x 7168,
-// eight slots and a shared expert, with norm, gate and residual 282 us (1.39 GB,
-// 4.9 TB/s); 64 rows of 4096 in 4.9 us, of which the launch takes 4.7.
+// Measured: norm of 8192 x 7168 fp32 to bf16 71.5 us (352 MB, 4.9 TB/s, a device copy
+// 4.7), to bf16 and codes 82.5 us (411 MB, 5.0 TB/s), of bf16 to both 64 us (294 MB,
+// 4.6 TB/s); 65536 x 1024 fp16 to codes 41 us (4.9 TB/s); combine of 8192 x 7168, eight
+// slots and a shared expert, with norm, gate and residual 282 us (1.39 GB, 4.9
+// TB/s); 64 rows of 4096 in 4.9 us, of which the launch takes 4.7.
 #include "moe_internal.h"
 #include "quant_int8.h"
 #include "swiglu.h"
@@ -235,9 +236,10 @@ hipError_t launch_rows(int rows, int cols, const void* x, const float* weight, f
   hipLaunchKernelGGL((k_rows<DT, V, NT, NORM>), row_grid(rows), dim3(NT), 0, st, rows, cols, x, weight, eps, \
                      out_dtype == MOE_BF16 ? 1 : 0, out, static_cast<uint8_t*>(codes), scales, rows_dev, h_flags)
   // many short rows to quantise: a wavefront each, without the block's barrier
-  // (65536 rows of 1024 fp16 39 against 58 us, of 2048 85 against 91); fewer or
-  // longer ones, and the norm with its weight: a block each (8192 rows of 2048
-  // fp32: 14 against 16 us)
+  // (65536 rows of 1024 fp16 41 against 60 us, of 2048 73 against 83; 16384 rows 11.1
+  // against 14.7 and 21.5 against 21.7); fewer or longer ones, and the norm with its
+  // weight: a block each (norm of 8192 rows of 2048 fp32 17.1 us either way; of 1024
+  // a wavefront each would be 9.6 against 11.0)
   const bool waves = !NORM && rows >= 16384;
   if (granules <= 64) MOE_ROWS(1, 64);
   else if (waves && granules <= 128) MOE_ROWS(2, 64);

@@ -479,7 +479,9 @@ __device__ __forceinline__ void gemm_tile(
     constexpr int RW = kPingRowElems;
     // 32- and 64-row tiles (small experts): each weight row is read by one or
     // two row tiles only, so its loads are non-temporal and do not displace
-    // the L2 lines that the big tiles of an interleaved launch reuse
+    // the L2 lines that the big tiles of an interleaved launch reuse.  (Not so
+    // for the 64-row rests and quarters of k_gemm_rows_i8, whose neighbours read
+    // the same weight rows: what normal loads would give there is not measured.)
     constexpr bool STREAM_W = BM <= 64;
     constexpr int PSTAGE = ROWS * RW;   // elements of one stage
     constexpr int NI = ROWS / (8 * NW); // 8-row loads per wave per stage
