@@ -276,3 +276,6 @@ def test_helpers_on_a_given_stream_own_their_memory():
         got = make(side.cuda_stream)
         torch.cuda.synchronize()
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+        got = make(torch.cuda.default_stream().cuda_stream)   # (0)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
