@@ -166,7 +166,7 @@ def prepare(case, seed):
     else:
         H, I, E, rows = c["hidden"], c["inter"], c["experts"], c["tokens"] * c["k"]
         s["x"] = (_randn(gen, rows, H) * 150).clamp_(-TOP, TOP).to(FP8)
-        s["x_scales"] = (1 + 0.2 * _rand(gen, H // B, rows)) / 150
+        s["x_scales"] = (1 + 0.2 * _rand(gen, rows, H // B)) / 150
         s["gate"], s["gate_scales"] = _weights(gen, E, I, H)
         s["up"], s["up_scales"] = _weights(gen, E, I, H)
         s["down"], s["down_scales"] = _weights(gen, E, H, I)
@@ -197,10 +197,10 @@ def _handles(s):
         else:
             s["code"] = code[c["type"]]
             s["perm"] = zeros(T * k, H, dtype=torch.uint8 if c["codes"] else DTYPES[c["type"]])
-            s["scales"] = zeros(H // B, T * k, dtype=torch.float32) if c["codes"] else None
+            s["scales"] = zeros(T * k, H // B, dtype=torch.float32) if c["codes"] else None
     elif c["op"] == "product":
         s["codes"] = zeros(c["rows"], c["k"], dtype=torch.uint8)
-        s["scales"] = zeros(c["k"] // B, c["rows"], dtype=torch.float32)
+        s["scales"] = zeros(c["rows"], c["k"] // B, dtype=torch.float32)
         s["y"], s["code"] = zeros(c["rows"], c["n"], dtype=DTYPES[c["out"]]), code[c["out"]]
         s["ws"] = zeros(abi.moe_workspace_size_gemm_fp8(c["rows"], c["n"], c["k"], c["experts"]), dtype=torch.uint8)
     else:
@@ -228,7 +228,7 @@ def _run_own(s):
     if c["op"] == "sort":
         n = c["tokens"] * c["k"]
         if c["codes"]:
-            abi.moe_dispatch_rows_fp8(s["shape"], s["code"], s["x"], s["rows"], n, n, s["perm"], s["scales"])
+            abi.moe_dispatch_rows_fp8(s["shape"], s["code"], s["x"], s["rows"], n, s["perm"], s["scales"])
             return {"codes": s["perm"].view(FP8), "scales": s["scales"]}
         abi.moe_dispatch_rows(s["shape"], s["code"], s["x"], s["rows"], s["gates"] if c["weights"] else None, n,
                               s["perm"])
@@ -244,21 +244,20 @@ def _run_own(s):
                                  c["tokens"] * c["k"], s["dy"], s["dg"])
         return {"dy": s["dy"], "dg": s["dg"]}
     if c["op"] == "product":
-        abi.moe_quantize_fp8(c["rows"], c["k"], abi.MOE_BF16, s["x"], c["rows"], s["codes"], s["scales"])
-        abi.moe_grouped_gemm_fp8(c["rows"], c["n"], c["k"], c["experts"], s["codes"], s["scales"], c["rows"],
-                                 s["offsets"], s["w"], s["w_scales"], s["code"], s["y"], s["ws"])
+        abi.moe_quantize_fp8(c["rows"], c["k"], abi.MOE_BF16, s["x"], s["codes"], s["scales"])
+        abi.moe_grouped_gemm_fp8(c["rows"], c["n"], c["k"], c["experts"], s["codes"], s["scales"], s["offsets"],
+                                 s["w"], s["w_scales"], s["code"], s["y"], s["ws"])
         return {"scales": s["scales"], "out": s["y"]}
-    abi.moe_grouped_ffn_fp8(s["shape"], s["x"], s["x_scales"], c["tokens"] * c["k"], s["offsets"], s["weights"],
-                            s["code"], s["y"], s["ws"])
+    abi.moe_grouped_ffn_fp8(s["shape"], s["x"], s["x_scales"], s["offsets"], s["weights"], s["code"], s["y"], s["ws"])
     return {"out": s["y"]}
 
 
 def _quantise(x):
-    """Codes of x [R, K] fp32 by blocks of 128 columns, and the scales [K / 128, R]."""
+    """Codes of x [R, K] fp32 by blocks of 128 columns, and the scales [R, K / 128]."""
     v = x.view(x.shape[0], -1, B)
     top = v.abs().amax(2, keepdim=True)
     codes = torch.where(top > 0, TOP * v / top, 0.0).to(FP8)
-    return codes.view(x.shape), (top / TOP).squeeze(2).t().contiguous()
+    return codes.view(x.shape), (top / TOP).squeeze(2)
 
 
 def _sort(s):
@@ -271,8 +270,8 @@ def _sort(s):
         codes, scales = _quantise(x)
         out = torch.zeros(T * k, H, dtype=torch.uint8, device="cuda")
         out[to] = codes.view(torch.uint8)[token]
-        out_scales = torch.zeros(H // B, T * k, device="cuda")
-        out_scales[:, to] = scales[:, token]
+        out_scales = torch.zeros(T * k, H // B, device="cuda")
+        out_scales[to] = scales[token]
         return {"codes": out.view(FP8), "scales": out_scales}
     out = torch.zeros(T * k, H, dtype=s["x"].dtype, device="cuda")
     moved = x[token]
@@ -322,7 +321,7 @@ def _grouped(a, w, scales, offsets, most):
 
 
 def _decode(codes, scales):
-    v = codes.float().view(codes.shape[0], -1, B) * scales.t().unsqueeze(2)
+    v = codes.float().view(codes.shape[0], -1, B) * scales.unsqueeze(2)
     return v.view(codes.shape)
 
 
@@ -406,7 +405,7 @@ def _exact_sort(s):
             out[r[ok]] = v[ok].to(wide)  # codes are exact in fp32
             if c["codes"]:
                 scales[r[ok]] = sc[ok]
-    return {"codes": out, "scales": scales.t().contiguous()} if c["codes"] else {"rows": out}
+    return {"codes": out, "scales": scales} if c["codes"] else {"rows": out}
 
 
 def _exact_unsort(s):
@@ -454,12 +453,12 @@ def _exact_times(x, sx, w, sw):
 def _exact_product(s):
     codes, scales = _exact_codes(s["x"].double())
     y = _exact_groups(s, lambda e, r: _exact_times(codes[r], scales[r], s["w"][e], s["w_scales"][e]))
-    return {"scales": scales.t().contiguous(), "out": y}
+    return {"scales": scales, "out": y}
 
 
 def _exact_ffn(s):
     def one(e, r):
-        x, sx = s["x"][r].double(), s["x_scales"][:, r].t().double()
+        x, sx = s["x"][r].double(), s["x_scales"][r].double()
         g = _exact_times(x, sx, s["gate"][e], s["gate_scales"][e])
         u = _exact_times(x, sx, s["up"][e], s["up_scales"][e])
         return _exact_times(*_exact_codes(g * torch.sigmoid(g) * u), s["down"][e], s["down_scales"][e])
