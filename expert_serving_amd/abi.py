@@ -28,7 +28,9 @@ EXPORTED = ("moe_workspace_size", "moe_route_topk", "moe_dispatch", "moe_map_rep
             "moe_ep_dispatch_layout", "moe_ep_combine", "moe_convert_bf16_to_f16", "moe_route_biased",
             "moe_quantize_int8", "moe_workspace_size_gemm_int8", "moe_grouped_gemm_int8", "moe_workspace_size_int8",
             "moe_grouped_ffn_int8", "moe_norm", "moe_combine_norm", "moe_workspace_size_block", "moe_block_forward",
-            "moe_block_forward_int8")
+            "moe_block_forward_int8", "moe_quantize_fp8", "moe_quantize_fp8_weights", "moe_workspace_size_gemm_fp8",
+            "moe_grouped_gemm_fp8", "moe_workspace_size_fp8", "moe_grouped_ffn_fp8", "moe_dispatch_rows",
+            "moe_dispatch_rows_fp8", "moe_dispatch_rows_backward", "moe_combine_backward")
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -65,6 +67,13 @@ class MoeMxfp8Ffn(ctypes.Structure):
 
 class MoeInt8Ffn(ctypes.Structure):
     """moe_int8_ffn: int8 codes and per-channel scales of the gate, up and down weights."""
+    _fields_ = [("gate", ctypes.c_void_p), ("gate_scales", ctypes.c_void_p),
+                ("up", ctypes.c_void_p), ("up_scales", ctypes.c_void_p),
+                ("down", ctypes.c_void_p), ("down_scales", ctypes.c_void_p)]
+
+
+class MoeFp8Ffn(ctypes.Structure):
+    """moe_fp8_ffn: E4M3 codes and 128 x 128 block scales of the gate, up and down weights."""
     _fields_ = [("gate", ctypes.c_void_p), ("gate_scales", ctypes.c_void_p),
                 ("up", ctypes.c_void_p), ("up_scales", ctypes.c_void_p),
                 ("down", ctypes.c_void_p), ("down_scales", ctypes.c_void_p)]
@@ -137,6 +146,16 @@ def lib():
         L.moe_workspace_size_block.argtypes = [sp, szp]
         L.moe_block_forward.argtypes = [sp, bp] + [vp] * 11 + [ctypes.POINTER(MoeDebug), vp, sz, vp]
         L.moe_block_forward_int8.argtypes = [sp, bp, vp, vp, vp, vp, fp, fp, vp, ctypes.POINTER(MoeDebug), vp, sz, vp]
+        L.moe_quantize_fp8.argtypes = [i32, i32, i32, vp, vp, vp, vp]
+        L.moe_quantize_fp8_weights.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp]
+        L.moe_workspace_size_gemm_fp8.argtypes = [i32, i32, i32, i32, szp]
+        L.moe_grouped_gemm_fp8.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]
+        L.moe_workspace_size_fp8.argtypes = [sp, szp]
+        L.moe_grouped_ffn_fp8.argtypes = [sp, vp, vp, vp, ctypes.POINTER(MoeFp8Ffn), i32, vp, vp, sz, vp]
+        L.moe_dispatch_rows.argtypes = [sp, i32, vp, vp, vp, i32, vp, vp]
+        L.moe_dispatch_rows_fp8.argtypes = [sp, i32, vp, vp, i32, vp, vp, vp]
+        L.moe_dispatch_rows_backward.argtypes = [sp, i32, vp, vp, i32, vp, vp, vp, vp, vp]
+        L.moe_combine_backward.argtypes = [sp, i32, vp, i32, vp, vp, vp, i32, vp, vp, vp]
         for name in EXPORTED:
             if name not in ("moe_status_string", "moe_last_hip_error"):
                 getattr(L, name).restype = st
@@ -528,3 +547,108 @@ def moe_block_forward_int8(shape, block, x, w_router, router_bias, k_per_token, 
                                         ctypes.byref(d) if d is not None else None, _ptr(ws),
                                         ws.numel() if ws_bytes is None else ws_bytes, _stream(stream)),
            "moe_block_forward_int8")
+
+
+# ---- experts on 8-bit floating-point blocks of 128, rows to expert order, gradients ----
+
+def moe_quantize_fp8(rows, cols, src_dtype, src, codes, scales, stream=None):
+    _check(lib().moe_quantize_fp8(int(rows), int(cols), int(src_dtype), _ptr(src), _ptr(codes), _ptr(scales),
+                                  _stream(stream)), "moe_quantize_fp8")
+
+
+def moe_quantize_fp8_weights(num_experts, n, k, src_dtype, src, codes, scales, stream=None):
+    _check(lib().moe_quantize_fp8_weights(int(num_experts), int(n), int(k), int(src_dtype), _ptr(src), _ptr(codes),
+                                          _ptr(scales), _stream(stream)), "moe_quantize_fp8_weights")
+
+
+def _to_quantise(t, stream):
+    """(moe_dtype, t contiguous) of a bf16, fp32 or fp16 tensor, contiguous already when a stream is given."""
+    import torch
+    if stream is not None and not t.is_contiguous():
+        raise ValueError("a tensor quantised on a given stream has to be contiguous")
+    return {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}[t.dtype], t.contiguous()
+
+
+def quantize_fp8(t, stream=None):
+    """(codes float8_e4m3fn of t's shape, scales fp32 [..., K / 128]) of a bf16, fp32 or fp16 device tensor of rows
+    (contiguous when a stream is given, on which codes and scales are then allocated)."""
+    import torch
+    dt, t = _to_quantise(t, stream)
+    K = t.shape[-1]
+    with _tensors_on(stream, t.device):
+        codes = torch.empty(t.shape, dtype=torch.float8_e4m3fn, device=t.device)
+        scales = torch.empty(*t.shape[:-1], K // 128, dtype=torch.float32, device=t.device)
+        moe_quantize_fp8(t.numel() // K if K else 0, K, dt, t, codes, scales, stream)
+    return codes, scales
+
+
+def quantize_fp8_weights(t, stream=None):
+    """(codes float8_e4m3fn of t's shape, scales fp32 [..., ceil(N / 128), K / 128]) of weights [N, K] or [E, N, K]."""
+    import torch
+    dt, t = _to_quantise(t, stream)
+    N, K = t.shape[-2:]
+    experts = t.shape[0] if t.dim() == 3 else 1
+    with _tensors_on(stream, t.device):
+        codes = torch.empty(t.shape, dtype=torch.float8_e4m3fn, device=t.device)
+        scales = torch.empty(*t.shape[:-2], -(-N // 128), K // 128, dtype=torch.float32, device=t.device)
+        moe_quantize_fp8_weights(experts, N, K, dt, t, codes, scales, stream)
+    return codes, scales
+
+
+def fp8_ffn(gate, up, down):
+    """One FFN's weights from (codes, scales) pairs (routed [E][I][H] / [E][H][I] with scales [E][I/128][H/128] /
+    [E][H/128][I/128]): a dict of the device tensors plus the struct under "abi"."""
+    st = MoeFp8Ffn(*(_ptr(t) for pair in (gate, up, down) for t in pair))
+    return dict(gate=gate, up=up, down=down, abi=st)
+
+
+def moe_workspace_size_gemm_fp8(rows, n, k, num_experts) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().moe_workspace_size_gemm_fp8(int(rows), int(n), int(k), int(num_experts), ctypes.byref(b)),
+           "moe_workspace_size_gemm_fp8")
+    return int(b.value)
+
+
+def moe_grouped_gemm_fp8(rows, n, k, num_experts, a, a_scales, expert_offsets, b, b_scales, y_dtype, y, ws,
+                         ws_bytes=None, stream=None):
+    _check(lib().moe_grouped_gemm_fp8(int(rows), int(n), int(k), int(num_experts), _ptr(a), _ptr(a_scales),
+                                      _ptr(expert_offsets), _ptr(b), _ptr(b_scales), int(y_dtype), _ptr(y),
+                                      _ptr(ws), ws.numel() if ws_bytes is None else ws_bytes, _stream(stream)),
+           "moe_grouped_gemm_fp8")
+
+
+def moe_workspace_size_fp8(shape: MoeShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_workspace_size_fp8(ctypes.byref(shape), ctypes.byref(n)), "moe_workspace_size_fp8")
+    return int(n.value)
+
+
+def moe_grouped_ffn_fp8(shape, x_codes, x_scales, expert_offsets, experts, y_dtype, y_perm, ws, ws_bytes=None,
+                        stream=None):
+    _check(lib().moe_grouped_ffn_fp8(ctypes.byref(shape), _ptr(x_codes), _ptr(x_scales), _ptr(expert_offsets),
+                                     _mx(experts), int(y_dtype), _ptr(y_perm), _ptr(ws),
+                                     ws.numel() if ws_bytes is None else ws_bytes, _stream(stream)),
+           "moe_grouped_ffn_fp8")
+
+
+def moe_dispatch_rows(shape, dtype, x, row_of_slot, weights, num_rows, x_perm, stream=None):
+    _check(lib().moe_dispatch_rows(ctypes.byref(shape), int(dtype), _ptr(x), _ptr(row_of_slot), _ptr(weights),
+                                   int(num_rows), _ptr(x_perm), _stream(stream)), "moe_dispatch_rows")
+
+
+def moe_dispatch_rows_fp8(shape, dtype, x, row_of_slot, num_rows, x_codes, x_scales, stream=None):
+    _check(lib().moe_dispatch_rows_fp8(ctypes.byref(shape), int(dtype), _ptr(x), _ptr(row_of_slot), int(num_rows),
+                                       _ptr(x_codes), _ptr(x_scales), _stream(stream)), "moe_dispatch_rows_fp8")
+
+
+def moe_dispatch_rows_backward(shape, dtype, d_perm, row_of_slot, num_rows, weights, x, d_x, d_weights, stream=None):
+    _check(lib().moe_dispatch_rows_backward(ctypes.byref(shape), int(dtype), _ptr(d_perm), _ptr(row_of_slot),
+                                            int(num_rows), _ptr(weights), _ptr(x), _ptr(d_x), _ptr(d_weights),
+                                            _stream(stream)), "moe_dispatch_rows_backward")
+
+
+def moe_combine_backward(shape, out_dtype, d_out, y_dtype, y_perm, row_of_slot, topk_gates, num_rows, d_y, d_gates,
+                         stream=None):
+    _check(lib().moe_combine_backward(ctypes.byref(shape), int(out_dtype), _ptr(d_out), int(y_dtype), _ptr(y_perm),
+                                      _ptr(row_of_slot), _ptr(topk_gates), int(num_rows), _ptr(d_y), _ptr(d_gates),
+                                      _stream(stream)), "moe_combine_backward")

@@ -135,6 +135,26 @@ moe_status check_int8_ffn(const moe_int8_ffn* w) {
   return MOE_OK;
 }
 
+// layers on 8-bit floating-point blocks: as int8 ones, without their limit of K
+moe_status check_fp8_shape(const moe_shape* s) {
+  MOE_TRY(check_shape(s));
+  if (s->act_dtype != MOE_BF16 || s->down_dtype == MOE_F16) return MOE_ERR_UNSUPPORTED;
+  if (s->hidden % 128 || s->intermediate % 128) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_fp8_ffn(const moe_fp8_ffn* w) {
+  if (!w) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(w->gate));
+  MOE_TRY(need4(w->gate_scales));
+  MOE_TRY(need(w->up));
+  MOE_TRY(need4(w->up_scales));
+  MOE_TRY(need(w->down));
+  MOE_TRY(need4(w->down_scales));
+  return MOE_OK;
+}
+
+inline bool is_half_type(int dt) { return dt == MOE_F16 || dt == MOE_BF16; }
 inline bool is_float_type(int dt) { return dt == MOE_F32 || dt == MOE_F16 || dt == MOE_BF16; }
 inline bool is_stream_type(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 inline moe_status opt16(const void* p) { return p ? need(p) : MOE_OK; }
@@ -819,6 +839,71 @@ moe_status check_gemm_i8(int32_t rows, int32_t n, int32_t k, int32_t E) {
   if ((long long)n * k > (long long)INT_MAX || (long long)E * n > (long long)INT_MAX || rows > INT_MAX / 2)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
+}
+
+// ---- products on 8-bit floating-point blocks ------------------------------------
+moe_status check_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t E) {
+  if (rows < 0 || n <= 0 || k <= 0 || E < 1) return MOE_ERR_INVALID_ARG;
+  if (E > kMaxExperts || n % 16 || k % 128) return MOE_ERR_UNSUPPORTED;
+  if ((long long)n * k > (long long)INT_MAX || (long long)E * n > (long long)INT_MAX || rows > INT_MAX / 2)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+struct Fp8Plan {
+  GemmPlan gp;
+  int max_tiles;
+  size_t flags, sched, sched_count, h, hq, hsc, total;
+};
+
+// rows over E experts; inter > 0: an FFN's h of that many columns
+Fp8Plan plan_fp8(long long rows, int E, int inter) {
+  Fp8Plan p{};
+  p.gp.bm_big = p.gp.bm_small = kFp8TileRows;
+  p.gp.split_rows = 0;
+  p.max_tiles = (int)(rows / kFp8TileRows + E + 1);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at_ = o;
+    o = align_up(o + bytes, 256);
+    return at_;
+  };
+  p.flags = take(256);
+  p.sched = take((size_t)p.max_tiles * sizeof(MTile));
+  p.sched_count = take(16);
+  p.h = take((size_t)rows * inter * 4);
+  p.hq = take((size_t)rows * inter);
+  p.hsc = take((size_t)rows * (inter / 128) * 4);
+  p.total = o;
+  return p;
+}
+
+moe_status run_ffn_fp8(const moe_shape& s, const void* x, const float* xsc, const int32_t* offsets,
+                       const moe_fp8_ffn& w, int y_dtype, void* y, void* ws, const Fp8Plan& p, hipStream_t st) {
+  const int E = s.num_experts, H = s.hidden, I = s.intermediate, slots = s.num_tokens * s.top_k;
+  uint32_t* flags = at<uint32_t>(ws, p.flags);
+  MTile* sched = at<MTile>(ws, p.sched);
+  int32_t* count = at<int32_t>(ws, p.sched_count);
+  float* h = at<float>(ws, p.h);
+  uint8_t* hq = at<uint8_t>(ws, p.hq);
+  float* hsc = at<float>(ws, p.hsc);
+  MOE_HIP(launch_build_schedule(offsets, E, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags));
+  const Fp8Args up{static_cast<const uint8_t*>(x), xsc, H / 128, 1, static_cast<const uint8_t*>(w.gate),
+                   static_cast<const uint8_t*>(w.up), w.gate_scales, w.up_scales, I, H, h, MOE_F32, sched, count, 0,
+                   flags};
+  MOE_HIP(launch_gemm_fp8(up, true, p.max_tiles, st));
+  MOE_HIP(launch_quant_fp8(MOE_F32, h, slots, I, offsets + E, hq, hsc, st));
+  const Fp8Args down{hq, hsc, I / 128, 1, static_cast<const uint8_t*>(w.down), nullptr, w.down_scales, nullptr, H, I,
+                     y, y_dtype, sched, count, 0, flags};
+  MOE_HIP(launch_gemm_fp8(down, false, p.max_tiles, st));
+  return MOE_OK;
+}
+
+// The slots' rows of a call on token rows of a type, and the columns it can take.
+moe_status check_rows(const moe_shape& s, int dtype, const int32_t* row_of_slot, int32_t num_rows) {
+  if (!is_float_type(dtype) || num_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (s.hidden % (dtype == MOE_F32 ? 4 : 8)) return MOE_ERR_UNSUPPORTED;
+  return need4(row_of_slot);
 }
 
 // ---- the layer, shared by the workspace and the no-allocation entry points ---
@@ -1560,6 +1645,160 @@ moe_status moe_grouped_ffn_int8(const moe_shape* shape, const int8_t* x_codes, c
   if (split)
     MOE_HIP(launch_sum_parts(at<float>(ws, L.y), L.ksplit, (long long)slots * s.hidden, s.hidden,
                              expert_offsets + s.num_experts, slots, y_dtype, y_perm, flags, st));
+  return MOE_OK;
+}
+
+moe_status moe_quantize_fp8(int32_t rows, int32_t cols, int32_t src_dtype, const void* src, void* codes,
+                            float* scales, void* stream) {
+  if (rows < 0 || cols <= 0 || !is_float_type(src_dtype)) return MOE_ERR_INVALID_ARG;
+  if (cols % 128) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(need(src));
+  MOE_TRY(need(codes));
+  MOE_TRY(need4(scales));
+  if (rows == 0) return MOE_OK;
+  MOE_HIP(launch_quant_fp8(src_dtype, src, rows, cols, nullptr, codes, scales, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_quantize_fp8_weights(int32_t num_experts, int32_t n, int32_t k, int32_t src_dtype, const void* src,
+                                    void* codes, float* scales, void* stream) {
+  if (!is_float_type(src_dtype)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_gemm_fp8(0, n, k, num_experts));
+  if ((n + 127) / 128 > 65535) return MOE_ERR_UNSUPPORTED;  // (an axis of the launch)
+  MOE_TRY(need(src));
+  MOE_TRY(need(codes));
+  MOE_TRY(need4(scales));
+  MOE_HIP(launch_quant_fp8_weights(src_dtype, src, num_experts, n, k, codes, scales, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_workspace_size_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_experts, size_t* bytes) {
+  MOE_TRY(check_gemm_fp8(rows, n, k, num_experts));
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = plan_fp8(rows, num_experts, 0).total;
+  return MOE_OK;
+}
+
+moe_status moe_grouped_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_experts, const void* a,
+                                const float* a_scales, const int32_t* expert_offsets, const void* b,
+                                const float* b_scales, int32_t y_dtype, void* y, void* ws, size_t ws_bytes,
+                                void* stream) {
+  MOE_TRY(check_gemm_fp8(rows, n, k, num_experts));
+  if (!is_half_type(y_dtype)) return y_dtype == MOE_F32 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(a));
+  MOE_TRY(need4(a_scales));
+  if (!expert_offsets && num_experts != 1) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(opt4(expert_offsets));
+  MOE_TRY(need(b));
+  MOE_TRY(need4(b_scales));
+  MOE_TRY(need(y));
+  MOE_TRY(need(ws));
+  const Fp8Plan p = plan_fp8(rows, num_experts, 0);
+  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
+  if (rows == 0) return MOE_OK;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  uint32_t* flags = at<uint32_t>(ws, p.flags);
+  MTile* sched = expert_offsets ? at<MTile>(ws, p.sched) : nullptr;
+  int32_t* count = at<int32_t>(ws, p.sched_count);
+  if (expert_offsets)
+    MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags));
+  else
+    MOE_HIP(launch_clear_flags(flags, st));
+  const Fp8Args g{static_cast<const uint8_t*>(a), a_scales, k / 128, 1, static_cast<const uint8_t*>(b), nullptr,
+                  b_scales, nullptr, n, k, y, y_dtype, sched, count, rows, flags};
+  MOE_HIP(launch_gemm_fp8(g, false, p.max_tiles, st));
+  return MOE_OK;
+}
+
+moe_status moe_workspace_size_fp8(const moe_shape* shape, size_t* bytes) {
+  MOE_TRY(check_fp8_shape(shape));
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = plan_fp8((long long)shape->num_tokens * shape->top_k, shape->num_experts, shape->intermediate).total;
+  return MOE_OK;
+}
+
+moe_status moe_grouped_ffn_fp8(const moe_shape* shape, const void* x_codes, const float* x_scales,
+                               const int32_t* expert_offsets, const moe_fp8_ffn* experts, int32_t y_dtype,
+                               void* y_perm, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_fp8_shape(shape));
+  const moe_shape& s = *shape;
+  if (!is_half_type(y_dtype)) return y_dtype == MOE_F32 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(x_codes));
+  MOE_TRY(need4(x_scales));
+  MOE_TRY(need4(expert_offsets));
+  MOE_TRY(check_fp8_ffn(experts));
+  MOE_TRY(need(y_perm));
+  MOE_TRY(need(ws));
+  const Fp8Plan p = plan_fp8((long long)s.num_tokens * s.top_k, s.num_experts, s.intermediate);
+  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
+  if (s.num_tokens == 0) return MOE_OK;
+  return run_ffn_fp8(s, x_codes, x_scales, expert_offsets, *experts, y_dtype, y_perm, ws, p,
+                     static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_dispatch_rows(const moe_shape* shape, int32_t dtype, const void* x, const int32_t* row_of_slot,
+                             const float* weights, int32_t num_rows, void* x_perm, void* stream) {
+  MOE_TRY(check_shape(shape));
+  MOE_TRY(check_rows(*shape, dtype, row_of_slot, num_rows));
+  MOE_TRY(need(x));
+  MOE_TRY(opt4(weights));
+  MOE_TRY(need(x_perm));
+  if (shape->num_tokens == 0 || num_rows == 0) return MOE_OK;
+  MOE_HIP(launch_dispatch_rows(*shape, dtype, x, row_of_slot, weights, num_rows, x_perm,
+                               static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_dispatch_rows_fp8(const moe_shape* shape, int32_t dtype, const void* x, const int32_t* row_of_slot,
+                                 int32_t num_rows, void* x_codes, float* x_scales, void* stream) {
+  MOE_TRY(check_shape(shape));
+  MOE_TRY(check_rows(*shape, dtype, row_of_slot, num_rows));
+  if (shape->hidden % 128) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(need(x));
+  MOE_TRY(need(x_codes));
+  MOE_TRY(need4(x_scales));
+  if (shape->num_tokens == 0 || num_rows == 0) return MOE_OK;
+  MOE_HIP(launch_dispatch_rows_fp8(*shape, dtype, x, row_of_slot, num_rows, x_codes, x_scales,
+                                   static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_dispatch_rows_backward(const moe_shape* shape, int32_t dtype, const void* d_perm,
+                                      const int32_t* row_of_slot, int32_t num_rows, const float* weights,
+                                      const void* x, void* d_x, float* d_weights, void* stream) {
+  MOE_TRY(check_shape(shape));
+  MOE_TRY(check_rows(*shape, dtype, row_of_slot, num_rows));
+  if (!d_x && !d_weights) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(d_perm));
+  MOE_TRY(opt4(weights));
+  if (d_weights) {
+    if (!weights) return MOE_ERR_INVALID_ARG;
+    MOE_TRY(need(x));
+    MOE_TRY(need4(d_weights));
+  }
+  MOE_TRY(opt16(d_x));
+  if (shape->num_tokens == 0) return MOE_OK;
+  MOE_HIP(launch_dispatch_rows_backward(*shape, dtype, d_perm, row_of_slot, num_rows, weights, x, d_x, d_weights,
+                                        static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_combine_backward(const moe_shape* shape, int32_t out_dtype, const void* d_out, int32_t y_dtype,
+                                const void* y_perm, const int32_t* row_of_slot, const float* topk_gates,
+                                int32_t num_rows, void* d_y, float* d_gates, void* stream) {
+  MOE_TRY(check_shape(shape));
+  if (!is_float_type(out_dtype)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_rows(*shape, y_dtype, row_of_slot, num_rows));
+  if (out_dtype != MOE_F32 && shape->hidden % 8) return MOE_ERR_UNSUPPORTED;
+  if (!d_y && !d_gates) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(d_out));
+  MOE_TRY(need4(topk_gates));
+  MOE_TRY(opt16(d_y));
+  MOE_TRY(opt4(d_gates));
+  if (d_gates) MOE_TRY(need(y_perm));
+  if (shape->num_tokens == 0) return MOE_OK;
+  MOE_HIP(launch_combine_backward(*shape, out_dtype, d_out, y_dtype, y_perm, row_of_slot, topk_gates, num_rows, d_y,
+                                  d_gates, static_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
 

@@ -309,6 +309,51 @@ hipError_t launch_swiglu_parts_i8(const int32_t* parts, int nparts, long long pa
 hipError_t launch_sum_parts(const float* parts, int nparts, long long part_elems, int N, const int32_t* rows_dev,
                             int max_rows, int y_dtype, void* y, uint32_t* flags, hipStream_t st);
 
+// ---- 8-bit floating-point operands with a scale per block of 128 (gemm_fp8.hip) ------
+// Row codes A [rows][K] with fp32 scales (row r, group g at sa[r * sa_row + g *
+// sa_group]), weight codes B0 (and B1 for gate/up) [E][N][K] with one scale per 128 x
+// 128 block ([E][N / 128 up][K / 128]).  K a multiple of 128, N of 16.
+struct Fp8Args {
+  const uint8_t* A;
+  const float* sa;
+  long long sa_row, sa_group;
+  const uint8_t* B0;
+  const uint8_t* B1;
+  const float* sb0;
+  const float* sb1;
+  int N, K;
+  void* out;
+  int y_dtype;            // MOE_F16 or MOE_BF16 (one matrix); fp32 h (gate/up)
+  const MTile* sched;     // row tiles of kFp8TileRows; null: rows [0, static_rows) of expert 0
+  const int32_t* count;
+  int static_rows;
+  uint32_t* flags;
+};
+constexpr int kFp8TileRows = 64;
+hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, int max_tiles, hipStream_t st);
+
+// rows [rows][cols] (cols a multiple of 128) to codes and scales [rows][cols / 128];
+// rows at and beyond *rows_dev (nullable) are left alone
+hipError_t launch_quant_fp8(int src_dtype, const void* src, int rows, int cols, const int32_t* rows_dev, void* codes,
+                            float* scales, hipStream_t st);
+hipError_t launch_quant_fp8_weights(int src_dtype, const void* src, int experts, int n, int k, void* codes,
+                                    float* scales, hipStream_t st);
+
+// ---- rows to expert order and back (rows.hip) ---------------------------------------
+// rows named outside [0, num_rows) count as none; weights nullable
+hipError_t launch_dispatch_rows(const moe_shape& s, int dtype, const void* x, const int32_t* row_of_slot,
+                                const float* weights, int num_rows, void* out, hipStream_t st);
+hipError_t launch_dispatch_rows_fp8(const moe_shape& s, int dtype, const void* x, const int32_t* row_of_slot,
+                                    int num_rows, void* codes, float* scales, hipStream_t st);
+// d_weights (nullable) only with weights and x; d_x nullable with d_weights
+hipError_t launch_dispatch_rows_backward(const moe_shape& s, int dtype, const void* d_perm, const int32_t* row_of_slot,
+                                         int num_rows, const float* weights, const void* x, void* d_x,
+                                         float* d_weights, hipStream_t st);
+// d_y or d_gates may be null, y only without d_gates
+hipError_t launch_combine_backward(const moe_shape& s, int out_dtype, const void* d_out, int y_dtype, const void* y,
+                                   const int32_t* row_of_slot, const float* gates, int num_rows, void* d_y,
+                                   float* d_gates, hipStream_t st);
+
 // ---- norms around the layer (block.hip) ------------------------------------------
 hipError_t launch_norm(int rows, int cols, int src_dtype, const void* x, const float* weight, float eps,
                        int out_dtype, void* out, void* codes, float* scales, hipStream_t st);

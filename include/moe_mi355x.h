@@ -70,11 +70,12 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 #define MOE_FLAG_BAD_K 1u       /* some k_per_token[t] outside [1, top_k]: token routed nowhere */
 #define MOE_FLAG_BAD_EXPERT 2u  /* some topk_ids entry outside [-1, E): slot treated as unused  */
 #define MOE_FLAG_H_RANGE 4u     /* some SwiGLU activation h exceeded fp16 range (bf16 and int8
-                                   experts) or was not finite (MXFP8 experts; int8: or NaN)   */
+                                   experts) or was not finite (MXFP8 and fp8 experts; int8: or
+                                   NaN)                                                        */
 #define MOE_FLAG_BAD_REPLICA 8u /* a routed expert without a replica, or a replica id out of range */
 #define MOE_FLAG_Y_RANGE 16u    /* some expert output exceeded fp16 range inside a layer call
                                    (moe_layer_forward, moe_layer_forward_mxfp8), a block call or
-                                   an fp16 y of the int8 calls                                 */
+                                   an fp16 y of the int8 and fp8 calls                         */
 
 typedef struct {
   int32_t num_tokens;          /* T >= 0                                                  */
@@ -494,6 +495,114 @@ moe_status moe_workspace_size_int8(const moe_shape* shape, size_t* bytes);
 moe_status moe_grouped_ffn_int8(const moe_shape* shape, const int8_t* x_codes, const float* x_scales,
                                 const int32_t* expert_offsets, const moe_int8_ffn* experts, int32_t y_dtype,
                                 void* y_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- experts on 8-bit floating-point blocks of 128 ------------------------
+ * E4M3 codes (OCP FP8: largest finite 448, no infinities, 0x7F / 0xFF NaN) with
+ * one fp32 scale per block: 128 consecutive elements of a row along the axis the
+ * product sums over, 128 x 128 elements of a weight (N x K; the last block of N
+ * may be short):
+ *   scale = amax / 448, code = 448 v / amax rounded to the nearest E4M3 value,
+ *   ties to even (a block of zeros has scale 0 and codes 0);
+ *   y[r][n] = sum over blocks b of scale_a[r][b] * scale_b[n / 128][b] *
+ *             sum over k in b of code_a[r][k] * code_b[n][k].
+ * Row codes [rows][K], scales [rows][K / 128]; weight codes [E][N][K], scales
+ * [E][ceil(N / 128)][K / 128].  K is a multiple of 128, N of 16 (the calls with a
+ * shape: H and I multiples of 128, act_dtype MOE_BF16).
+ * The matrix units add the products of a group of codes after aligning them to
+ * the largest one, dropping what lies below about 2^-13 of it; the groups' sums
+ * go on in fp32.  Sums of codes of rounded normal values are off by 1.4e-5 of
+ * their norm for that (measured), far below half a step of the 16-bit types
+ * (fp16 2^-11, bf16 2^-8), so the products are written in those: y_dtype is
+ * MOE_F16 or MOE_BF16, MOE_F32 is MOE_ERR_UNSUPPORTED.
+ * A block with an infinity or NaN gets unspecified codes and a scale that is not
+ * finite (NaN for a NaN); a row of a product with such a scale, or with a NaN
+ * code, is NaN, as is a column of such a weight block.  A scale of 0 may count as
+ * the smallest positive number. */
+
+/* Quantises rows src [rows][cols] (MOE_BF16, MOE_F32 or MOE_F16; cols a multiple
+ * of 128). */
+moe_status moe_quantize_fp8(int32_t rows, int32_t cols, int32_t src_dtype, const void* src, void* codes,
+                            float* scales, void* stream);
+
+/* Quantises weights src [num_experts][n][k] by 128 x 128 blocks, once.  The
+ * gradient with respect to a product's rows is a product with the transposed
+ * weights: where n is a multiple of 128, their codes and scales are these,
+ * transposed. */
+moe_status moe_quantize_fp8_weights(int32_t num_experts, int32_t n, int32_t k, int32_t src_dtype, const void* src,
+                                    void* codes, float* scales, void* stream);
+
+/* Grouped product: for every expert e and row r in [expert_offsets[e],
+ * expert_offsets[e+1]), y[r] = a[r] . b[e]^T as above, rounded once to y_dtype.
+ * y [rows][n].  expert_offsets [num_experts + 1] as moe_dispatch writes them,
+ * expert_offsets[num_experts] <= rows; NULL with num_experts == 1 for all rows.
+ * Rows at or beyond expert_offsets[num_experts] are neither read nor written.  An
+ * fp16 y out of range sets MOE_FLAG_Y_RANGE in the workspace flag word (and is
+ * infinite).  Fewer rows can need the larger workspace: a caller of several sizes
+ * takes the largest of their workspaces, here as for the FFN. */
+moe_status moe_workspace_size_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_experts, size_t* bytes);
+moe_status moe_grouped_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_experts, const void* a,
+                                const float* a_scales, const int32_t* expert_offsets, const void* b,
+                                const float* b_scales, int32_t y_dtype, void* y, void* ws, size_t ws_bytes,
+                                void* stream);
+
+typedef struct {
+  const void* gate;          /* [E][I][H] codes               */
+  const float* gate_scales;  /* [E][I / 128][H / 128]         */
+  const void* up;            /* [E][I][H] codes               */
+  const float* up_scales;    /* [E][I / 128][H / 128]         */
+  const void* down;          /* [E][H][I] codes               */
+  const float* down_scales;  /* [E][H / 128][I / 128]         */
+} moe_fp8_ffn;
+
+/* S7-S8 on such operands: as moe_grouped_ffn, with x_perm given as codes
+ * [T*top_k][H] and scales [T*top_k][H / 128]; h = silu(a) * u in fp32 is quantised
+ * per row and block of 128 columns before the down projection (an h that is not
+ * finite sets MOE_FLAG_H_RANGE, and its y row is NaN); y_perm in y_dtype (an fp16
+ * value out of range sets MOE_FLAG_Y_RANGE).  Clears the workspace flag word. */
+moe_status moe_workspace_size_fp8(const moe_shape* shape, size_t* bytes);
+moe_status moe_grouped_ffn_fp8(const moe_shape* shape, const void* x_codes, const float* x_scales,
+                               const int32_t* expert_offsets, const moe_fp8_ffn* experts, int32_t y_dtype,
+                               void* y_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- rows to expert order, and the gradients of dispatch and combine --------
+ * For rows of any type (MOE_F32, MOE_BF16 or MOE_F16, whatever act_dtype is; H a
+ * multiple of 8, of 4 when every row of the call is fp32) given the permutation
+ * that moe_dispatch leaves in row_of_slot [T][top_k]; entries outside [0,
+ * num_rows) are slots without a row, the others are distinct.  num_rows is the
+ * rows that the permuted buffers hold.  Sums in fp32, in slot order, rounded once;
+ * no workspace. */
+
+/* x_perm[row_of_slot[t][j]] = weights[t][j] * x[t] (weights [T][top_k] fp32, NULL:
+ * 1).  Rows that no slot names are left as they were. */
+moe_status moe_dispatch_rows(const moe_shape* shape, int32_t dtype, const void* x, const int32_t* row_of_slot,
+                             const float* weights, int32_t num_rows, void* x_perm, void* stream);
+
+/* The same rows, unweighted, as the codes [num_rows][H] and scales [num_rows][H /
+ * 128] that moe_quantize_fp8 makes of x[t]: the input of moe_grouped_ffn_fp8 and
+ * moe_grouped_gemm_fp8.  H a multiple of 128; x in dtype. */
+moe_status moe_dispatch_rows_fp8(const moe_shape* shape, int32_t dtype, const void* x, const int32_t* row_of_slot,
+                                 int32_t num_rows, void* x_codes, float* x_scales, void* stream);
+
+/* The gradient of moe_dispatch_rows (and, without weights, of moe_dispatch's
+ * x_perm) from that of x_perm:
+ *   d_x[t]          = sum over j with a row of weights[t][j] * d_perm[row]     [T][H]
+ *   d_weights[t][j] = <d_perm[row], x[t]>, 0 for a slot without a row  [T][top_k] fp32
+ * weights NULL: 1, and d_weights NULL.  d_x may be NULL when d_weights is not; x is
+ * read only for d_weights (else it may be NULL). */
+moe_status moe_dispatch_rows_backward(const moe_shape* shape, int32_t dtype, const void* d_perm,
+                                      const int32_t* row_of_slot, int32_t num_rows, const float* weights,
+                                      const void* x, void* d_x, float* d_weights, void* stream);
+
+/* The gradient of moe_combine (and of the sum inside moe_combine_norm) from that
+ * of its output, d_out [T][H] in out_dtype (which is also y_shared's gradient):
+ *   d_y[row_of_slot[t][j]] = topk_gates[t][j] * d_out[t]        [num_rows][H] in y_dtype
+ *   d_gates[t][j] = <d_out[t], y_perm[row]>, 0 for a slot without a row  [T][top_k] fp32
+ * Rows of d_y that no slot names are left as they were.  d_y or d_gates may be NULL,
+ * not both; y_perm [num_rows][H] in y_dtype is read only for d_gates (else it may be
+ * NULL) and may be d_y itself. */
+moe_status moe_combine_backward(const moe_shape* shape, int32_t out_dtype, const void* d_out, int32_t y_dtype,
+                                const void* y_perm, const int32_t* row_of_slot, const float* topk_gates,
+                                int32_t num_rows, void* d_y, float* d_gates, void* stream);
 
 /* ---- the block around the layer ----------------------------------------
  * A transformer block's FFN half with the layer in it:
