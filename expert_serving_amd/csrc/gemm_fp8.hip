@@ -1,5 +1,28 @@
 // Products of 8-bit floating-point rows and expert weights with an fp32 scale per
-// block of 128 (the launchers and their operands: moe_internal.h).
+// block of 128 along K (and per 128 weight rows): y = sum over blocks b of
+// sa[r][b] sb[n / 128][b] sum_k a[r][k] w[n][k], and the SwiGLU of two of them.
+//
+// The scales change from block to block, so they cannot wait for the epilogue.  A
+// block's sum on its own would take registers for it beside the running sums, which a
+// 256 x 256 tile does not have.  So the running sums are held in units: a scale is
+// 2^e m with m in [1, 2); the matrix units apply 2^e themselves (E8M0 operands of
+// v_mfma_scale_f32_32x32x64_f8f6f4, 2^e of the token row and of the weight block), and
+// before the first MFMA of a block every sum is multiplied by the ratio of the last
+// block's m_row m_weight to this one's, a factor between 1/4 and 4 that cannot leave
+// fp32's range.  One multiplication per sum and block either way; the ratio carries
+// three roundings, so that a sum over K / 128 blocks is off by a few times K / 128
+// half steps of fp32, far below the 2^-13 that the units' alignment of products costs.
+//
+// One block of 8 wavefronts (two per SIMD) makes a tile of up to 256 token rows (in
+// steps of 64) x 256 weight rows (gate/up: 128 of each matrix), weights as the MFMA's
+// first operand, so that a lane's 16 sums of a fragment belong to one token row.  A
+// stage is K = 128 in one of two LDS buffers: rows of 128 bytes, 16-byte chunk c of
+// row r at c ^ ((r >> 1) & 7), filled straight from memory (8 rows x 128 bytes per
+// wavefront load).  A stage has two steps of K = 64.  In the first the fragments of
+// the second are read, which is the last use of the buffer; a barrier; in the second
+// the fragments of the next stage are read and the loads of the stage after it issued.
+#include <type_traits>
+
 #include "moe_internal.h"
 #include "quant_fp8.h"
 #include "swiglu.h"
@@ -10,7 +33,14 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef const __attribute__((address_space(1))) void* gbl_ptr_t;
+
+constexpr int kBufferRsrcWord3 = 0x00020000;  // raw buffer of gfx9-family GPUs, 32-bit data format
+constexpr int kStage = 128;                   // codes (bytes) of K per stage
+constexpr int kChunkStages = 8;               // stages whose scales lie in LDS together
 
 __device__ __forceinline__ uint32_t f16_bits(float f) { return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f); }
 __device__ __forceinline__ uint32_t bf16_bits(float f) {
@@ -27,11 +57,344 @@ __device__ __forceinline__ f32x16 mfma8(i32x8 a, i32x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
 }
 
+__device__ __forceinline__ void raw_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Logical index of this block among `real` tiles, XCD by XCD (block b runs on XCD
+// b % 8), so that every XCD gets a contiguous range; false behind the last.
+__device__ __forceinline__ bool xcd_index(int real, int& L) {
+  const int b = blockIdx.x;
+  const int per_xcd = (real + 7) >> 3;
+  const int slot = b >> 3;
+  if (slot >= per_xcd) return false;
+  L = (b & 7) * per_xcd + slot;
+  return L < real;
+}
+
+// scale 2^e m: m in [1, 2) with the scale's sign, and e as the exponent byte in the
+// word's top byte (a scale below fp32's normal range counts as 2^-127 m)
+__device__ __forceinline__ float scale_m(uint32_t w) { return __uint_as_float((w & 0x807FFFFFu) | 0x3F800000u); }
+__device__ __forceinline__ int scale_e(uint32_t w) { return (int)(w << 1); }
+
+constexpr int tile_lds(int BM, int BN) {
+  return 2 * (BM + BN) * kStage + 2 * kChunkStages * (BM + 64) * 4;
+}
+
+// BM token rows x BN weight rows (DUAL: BN / 2 of each matrix).
+template <int BM, int BN, bool DUAL>
+__device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const MTile t, int ni) {
+  constexpr int FM = BM / 64, FN = BN / 128;   // fragments of a wavefront: 2 x 4 wavefronts
+  constexpr int WM = BM / 2, WN = DUAL ? BN / 8 : BN / 4;  // its rows and columns (of each matrix)
+  constexpr int NI = FM + BN / 64;             // 8-row loads per wavefront and stage
+  constexpr int BUF = (BM + BN) * kStage;
+  constexpr int COLS = DUAL ? BN / 2 : BN;     // output columns
+  static_assert(!DUAL || BN == 256, "a block of h columns per tile");
+  const int N = a.N, K = a.K, S = K / kStage;
+  const int rows = t.rows, n0 = ni * COLS;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const int fr = lane & 31, fk = lane >> 5;
+
+  // ---- loads ----
+  const uint8_t* A0 = a.A + (size_t)t.row0 * K;
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(A0), 0,
+                                                                      (uint32_t)rows * (uint32_t)K, kBufferRsrcWord3);
+  const size_t eb = (size_t)t.expert * N * K;
+  const __amdgpu_buffer_rsrc_t rb0 = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.B0 + eb), 0,
+                                                                       (uint32_t)N * (uint32_t)K, kBufferRsrcWord3);
+  const __amdgpu_buffer_rsrc_t rb1 = DUAL ? __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.B1 + eb), 0,
+                                                                              (uint32_t)N * (uint32_t)K, kBufferRsrcWord3)
+                                          : rb0;
+  // lane l of a load fills position l % 8 of row l / 8, which holds chunk
+  // (l % 8) ^ ((row >> 1) & 7); the row's own eight start at a multiple of 8 rows
+  // that is odd or even with the wavefront
+  const int chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
+  int va[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) va[i] = min(8 * (wave + 8 * i) + (lane >> 3), rows - 1) * K + chunk * 16;
+  const int vb = (lane >> 3) * K + chunk * 16;
+  auto load = [&](int buf, int s, int i) {  // load i of stage s
+    uint8_t* dst = smem + buf * BUF + 8 * (wave + 8 * i) * kStage;
+    if (i < FM) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)dst, 16, va[i < FM ? i : 0], s * kStage, 0, 0);
+    } else {
+      const int w0 = 8 * (wave + 8 * (i - FM));  // weight row of the tile; N is a multiple of 8
+      const int col = min(n0 + (DUAL ? w0 & (COLS - 1) : w0), N - 8);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(DUAL && w0 >= COLS ? rb1 : rb0, (lds_ptr_t)dst, 16, vb,
+                                               col * K + s * kStage, 0, 0);
+    }
+  };
+  // the scales of stages 8 c .. 8 c + 7: wavefront w those of stage 8 c + w, BM token
+  // rows, then the weight blocks of the tile (two, in turn over the lanes)
+  float* const s_row = reinterpret_cast<float*>(smem + 2 * BUF);  // [2][8][BM]
+  float* const s_wgt = s_row + 2 * kChunkStages * BM;             // [2][8][64]
+  const int nblocks = (N + kFp8Block - 1) / kFp8Block;
+  const float* const swl = (DUAL && (lane & 1) ? a.sb1 : a.sb0) +
+                           ((size_t)t.expert * nblocks +
+                            min(n0 / kFp8Block + (DUAL ? 0 : lane & 1), nblocks - 1)) * S;
+  auto load_scales = [&](int c) {
+    const int g = min(kChunkStages * c + wave, S - 1), at = (c & 1) * kChunkStages + wave;
+    const float* p = a.sa + (size_t)t.row0 * a.sa_row + (size_t)g * a.sa_group;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      __builtin_amdgcn_global_load_lds((gbl_ptr_t)(p + (size_t)min(64 * i + lane, rows - 1) * a.sa_row),
+                                       (lds_ptr_t)(s_row + at * BM + 64 * i), 4, 0, 0);
+    __builtin_amdgcn_global_load_lds((gbl_ptr_t)(swl + g), (lds_ptr_t)(s_wgt + at * 64), 4, 0, 0);
+  };
+
+  // ---- fragments ----
+  // row r of the stage, chunks 4 h + fk and 4 h + 2 + fk: (r >> 1) & 7 is that of fr,
+  // since fragments start at multiples of 32 rows
+  const int swz = (fr >> 1) & 7;
+  const uint8_t* const fa = smem + (wm * WM + fr) * kStage;
+  const uint8_t* const fb = smem + (BM + (DUAL ? wn * WN : wn * WN) + fr) * kStage;
+  auto frag = [&](const uint8_t* row, int h) {
+    return cat8(*reinterpret_cast<const u32x4*>(row + (((4 * h + fk) ^ swz) << 4)),
+                *reinterpret_cast<const u32x4*>(row + (((4 * h + 2 + fk) ^ swz) << 4)));
+  };
+  auto frag_a = [&](int s, int h, int b) { return frag(fa + (s & 1) * BUF + b * 32 * kStage, h); };
+  auto frag_b = [&](int s, int h, int f) { return frag(fb + (s & 1) * BUF + f * (DUAL ? COLS : 32) * kStage, h); };
+
+  f32x16 acc[FN][FM];
+#pragma unroll
+  for (int f = 0; f < FN; ++f)
+#pragma unroll
+    for (int b = 0; b < FM; ++b)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[f][b][q] = 0.f;
+  i32x8 xa[FM], wf[2][FN];
+  float mt[FM], mw[FN], rt[FM], rw[FN];  // units of the sums, their change at the next stage
+  int et[FM], ew[FN];
+  uint32_t nt[FM], nw[FN];               // scale words of the next stage
+  auto read_scales = [&](int s) {
+    const int at = ((s / kChunkStages) & 1) * kChunkStages + s % kChunkStages;
+#pragma unroll
+    for (int b = 0; b < FM; ++b) nt[b] = __float_as_uint(s_row[at * BM + wm * WM + b * 32 + fr]);
+#pragma unroll
+    for (int f = 0; f < FN; ++f) nw[f] = __float_as_uint(s_wgt[at * 64 + (DUAL ? f : (wn * WN) / kFp8Block)]);
+  };
+  auto next_units = [&]() {
+#pragma unroll
+    for (int b = 0; b < FM; ++b) {
+      const float m = scale_m(nt[b]);
+      rt[b] = mt[b] * __builtin_amdgcn_rcpf(m);
+      mt[b] = m;
+    }
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+      const float m = scale_m(nw[f]);
+      rw[f] = mw[f] * __builtin_amdgcn_rcpf(m);
+      mw[f] = m;
+    }
+  };
+
+#pragma unroll
+  for (int b = 0; b < FM; ++b) mt[b] = 1.f;
+#pragma unroll
+  for (int f = 0; f < FN; ++f) mw[f] = 1.f;
+  load_scales(0);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) load(0, 0, i);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) load(1, min(1, S - 1), i);
+  __builtin_amdgcn_s_waitcnt(0);
+  raw_barrier();
+  read_scales(0);
+#pragma unroll
+  for (int f = 0; f < FN; ++f) wf[0][f] = frag_b(0, 0, f);
+#pragma unroll
+  for (int b = 0; b < FM; ++b) xa[b] = frag_a(0, 0, b);
+  next_units();
+
+  // no branch inside a stage: loads past the last one read it again, into the buffer
+  // that is not read any more
+  for (int c = 0; c < S; c += kChunkStages) {
+    load_scales(c / kChunkStages + 1);
+    for (int s = c; s < min(c + kChunkStages, S); ++s) {
+      // first step: the sums to this stage's units
+#pragma unroll
+      for (int b = 0; b < FM; ++b) et[b] = scale_e(nt[b]);
+#pragma unroll
+      for (int f = 0; f < FN; ++f) ew[f] = scale_e(nw[f]);
+#pragma unroll
+      for (int f = 0; f < FN; ++f) wf[1][f] = frag_b(s, 1, f);
+#pragma unroll
+      for (int b = 0; b < FM; ++b) {
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+          const float r = rt[b] * rw[f];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) acc[f][b][q] *= r;
+          acc[f][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[0][f], xa[b], acc[f][b], 0, 0, 3, ew[f], 3, et[b]);
+        }
+        xa[b] = frag_a(s, 1, b);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // every wavefront has this buffer's last fragments, and its loads of the next
+      // stage have landed
+      __builtin_amdgcn_s_waitcnt(0);
+      raw_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      read_scales(min(s + 1, S - 1));
+#pragma unroll
+      for (int f = 0; f < FN; ++f) wf[0][f] = frag_b(s + 1, 0, f);
+#pragma unroll
+      for (int b = 0; b < FM; ++b) {
+#pragma unroll
+        for (int f = 0; f < FN; ++f)
+          acc[f][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[1][f], xa[b], acc[f][b], 0, 0, 3, ew[f], 3, et[b]);
+        xa[b] = frag_a(s + 1, 0, b);
+#pragma unroll
+        for (int i = b * NI / FM; i < (b + 1) * NI / FM; ++i) load(s & 1, min(s + 2, S - 1), i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      next_units();
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0);
+  raw_barrier();
+
+  // ---- epilogue: sum q of fragment (f, b) is column 32 f + 8 (q / 4) + 4 fk + q % 4 of
+  // the wavefront (DUAL: of matrix f), token row 32 b + fr ----
+  bool range = false;
+  if constexpr (DUAL) {
+    // h, its codes by blocks of 128 columns: the tile's.  A wavefront holds 32 of them;
+    // their maxima meet in LDS.
+    uint32_t* const s_top = reinterpret_cast<uint32_t*>(smem);  // [4][BM]
+    float h[FM][16];
+#pragma unroll
+    for (int b = 0; b < FM; ++b) {
+      uint32_t top = 0u;
+      const float u0 = mt[b] * mw[0], u1 = mt[b] * mw[1];
+      const bool in = n0 + wn * WN < N;   // (N is a multiple of 128)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        h[b][q] = silu_mul_exact(acc[0][b][q] * u0, acc[1][b][q] * u1);
+        top = max(top, f8_magnitude(h[b][q]));
+      }
+      const auto both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+      top = max(top, (uint32_t)(fk ? both[0] : both[1]));
+      if (fk == 0) s_top[wn * BM + wm * WM + b * 32 + fr] = in ? top : 0u;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < FM; ++b) {
+      const int m = wm * WM + b * 32 + fr;
+      const uint32_t top = max(max(s_top[m], s_top[BM + m]), max(s_top[2 * BM + m], s_top[3 * BM + m]));
+      const float amax = __uint_as_float(top);
+      const F8Block blk = f8_block(amax);
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        w[q] = f8_pack4(f8_quotient(h[b][4 * q], blk), f8_quotient(h[b][4 * q + 1], blk),
+                        f8_quotient(h[b][4 * q + 2], blk), f8_quotient(h[b][4 * q + 3], blk));
+      const auto s02 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+      const auto s13 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+      if (m >= rows) continue;
+      range |= !(amax <= 3.402823466e38f);
+      *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.out) + (size_t)(t.row0 + m) * N + n0 + wn * WN + 16 * fk) =
+          u32x4{s02[0], s02[1], s13[0], s13[1]};
+      if (wn == 0 && fk == 0) a.out_scales[(size_t)(n0 / kFp8Block) * a.out_group + t.row0 + m] = f8_scale(amax);
+    }
+  } else {
+    // through LDS (16-byte chunks swizzled by row), stored as whole runs of a row
+    constexpr int WC = FN * 32, CH = WC / 8;
+    uint16_t* const part = reinterpret_cast<uint16_t*>(smem) + wave * (WM * WC);
+    auto place = [&](int row, int ch) { return row * WC + ((ch ^ (CH == 8 ? row & 7 : (row >> 1) & 3)) << 3); };
+#pragma unroll
+    for (int b = 0; b < FM; ++b) {
+      const bool real = wm * WM + b * 32 + fr < rows;
+#pragma unroll
+      for (int f = 0; f < FN; ++f) {
+        const float u = mt[b] * mw[f];
+#pragma unroll
+        for (int qi = 0; qi < 4; ++qi) {
+          const bool in = n0 + wn * WC + f * 32 + 8 * qi < N;
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float v = acc[f][b][4 * qi + q] * u;
+            if (a.y_dtype == MOE_F16) {
+              range |= real && in && !(fabsf(v) <= 65504.f);
+              w[q] = f16_bits(v);
+            } else {
+              w[q] = bf16_bits(v);
+            }
+          }
+          *reinterpret_cast<u32x2*>(part + place(b * 32 + fr, f * 4 + qi) + 4 * fk) =
+              u32x2{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    constexpr int RPL = 64 / CH;
+#pragma unroll
+    for (int i = 0; i < WM / RPL; ++i) {
+      const int r = i * RPL + lane / CH, ch = lane % CH;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(part + place(r, ch));
+      const int m = wm * WM + r, n = n0 + wn * WC + 8 * ch;
+      if (m < rows && n < N)
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + (size_t)(t.row0 + m) * N + n) = v;
+    }
+  }
+  if (range && a.flags) atomicOr(a.flags, (uint32_t)(DUAL ? MOE_FLAG_H_RANGE : MOE_FLAG_Y_RANGE));
+}
+
+// Row tiles of up to 256 rows, each at the height its rows need; the blocks of an
+// expert's neighbouring row tiles come column by column (see the int8 form of the
+// same order).
+template <int BN, bool DUAL>
+__global__ __launch_bounds__(512) void k_gemm_fp8(const Fp8Args a, int mslots, int ntiles) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int mtiles = a.sched ? min(*a.count, mslots) : mslots;
+  int L;
+  if (!xcd_index(mtiles * ntiles, L)) return;
+  const int at = L / ntiles;
+  int first, size;
+  if (a.sched) {
+    const int group = a.sched[at].group;
+    first = at - (group & 0xFF), size = group >> 8;
+  } else {
+    first = at / kTileGroup * kTileGroup, size = min(kTileGroup, mtiles - first);
+  }
+  const int r = L - first * ntiles, col = r / size, i = first + (r - col * size);
+  MTile t;
+  if (a.sched) t = a.sched[i];
+  else t = MTile{0, 256 * i, min(256, a.static_rows - 256 * i), 0};
+  if (t.rows <= 0) return;
+  if (t.rows <= 64) tile_fp8<64, BN, DUAL>(smem, a, t, col);
+  else if (t.rows <= 128) tile_fp8<128, BN, DUAL>(smem, a, t, col);
+  else if (t.rows <= 192) tile_fp8<192, BN, DUAL>(smem, a, t, col);
+  else tile_fp8<256, BN, DUAL>(smem, a, t, col);
+}
+
+template <int BN, bool DUAL>
+hipError_t launch_tiles(const Fp8Args& a, int max_tiles, hipStream_t st) {
+  const int mslots = a.sched ? max_tiles : (a.static_rows + 255) / 256;
+  if (mslots <= 0) return hipSuccess;
+  constexpr int lds = tile_lds(256, BN);
+  static_assert(lds <= 160 * 1024, "LDS");
+  static std::atomic<uint64_t> set_on{0};
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(&k_gemm_fp8<BN, DUAL>), lds, set_on);
+  if (e != hipSuccess) return e;
+  constexpr int cols = DUAL ? BN / 2 : BN;
+  const int ntiles = (a.N + cols - 1) / cols;
+  const long long grid = ((long long)mslots * ntiles + 7) / 8 * 8;
+  if (grid > 0x7fffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((k_gemm_fp8<BN, DUAL>), dim3((unsigned)grid), dim3(512), lds, st, a, mslots, ntiles);
+  return hipGetLastError();
+}
+
 // 64 x 64 outputs per block of four wavefronts, a quarter each, operands straight from
 // memory.  A block of K = 128 is two MFMAs into a sum of its own, which the scales'
 // product then adds to the running one.
 template <bool DUAL>
-__global__ __launch_bounds__(256) void k_gemm_fp8(const Fp8Args a) {
+__global__ __launch_bounds__(256) void k_gemm_fp8_few(const Fp8Args a) {
   int expert = 0, row0 = blockIdx.y * kFp8TileRows, rows;
   if (a.sched) {
     if ((int)blockIdx.y >= *a.count) return;
@@ -109,14 +472,18 @@ __global__ __launch_bounds__(256) void k_gemm_fp8(const Fp8Args a) {
 }  // namespace
 
 hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, int max_tiles, hipStream_t st) {
+  return dual ? launch_tiles<256, true>(a, max_tiles, st) : launch_tiles<256, false>(a, max_tiles, st);
+}
+
+hipError_t launch_gemm_fp8_few(const Fp8Args& a, bool dual, int max_tiles, hipStream_t st) {
   const int tiles = a.sched ? max_tiles : (a.static_rows + kFp8TileRows - 1) / kFp8TileRows;
   if (tiles <= 0) return hipSuccess;
   if (tiles > 65535) return hipErrorInvalidValue;
   const dim3 grid((a.N + 63) / 64, tiles);
   if (dual)
-    hipLaunchKernelGGL(k_gemm_fp8<true>, grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL(k_gemm_fp8_few<true>, grid, dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL(k_gemm_fp8<false>, grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL(k_gemm_fp8_few<false>, grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

@@ -135,9 +135,12 @@ moe_status check_int8_ffn(const moe_int8_ffn* w) {
   return MOE_OK;
 }
 
-// layers on 8-bit floating-point blocks: as int8 ones, without their limit of K
+// layers on 8-bit floating-point blocks: as int8 ones; a row tile's offsets fit 32 bits
+constexpr int kMaxFp8K = 1 << 20;
+
 moe_status check_fp8_shape(const moe_shape* s) {
   MOE_TRY(check_shape(s));
+  if (s->hidden > kMaxFp8K || s->intermediate > kMaxFp8K) return MOE_ERR_UNSUPPORTED;
   if (s->act_dtype != MOE_BF16 || s->down_dtype == MOE_F16) return MOE_ERR_UNSUPPORTED;
   if (s->hidden % 128 || s->intermediate % 128) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
@@ -844,7 +847,7 @@ moe_status check_gemm_i8(int32_t rows, int32_t n, int32_t k, int32_t E) {
 // ---- products on 8-bit floating-point blocks ------------------------------------
 moe_status check_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t E) {
   if (rows < 0 || n <= 0 || k <= 0 || E < 1) return MOE_ERR_INVALID_ARG;
-  if (E > kMaxExperts || n % 16 || k % 128) return MOE_ERR_UNSUPPORTED;
+  if (E > kMaxExperts || n % 16 || k % 128 || k > kMaxFp8K) return MOE_ERR_UNSUPPORTED;
   if ((long long)n * k > (long long)INT_MAX || (long long)E * n > (long long)INT_MAX || rows > INT_MAX / 2)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
@@ -852,6 +855,7 @@ moe_status check_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t E) {
 
 struct Fp8Plan {
   GemmPlan gp;
+  bool few;
   int max_tiles;
   size_t flags, sched, sched_count, h, hq, hsc, total;
 };
@@ -859,9 +863,11 @@ struct Fp8Plan {
 // rows over E experts; inter > 0: an FFN's h of that many columns
 Fp8Plan plan_fp8(long long rows, int E, int inter) {
   Fp8Plan p{};
-  p.gp.bm_big = p.gp.bm_small = kFp8TileRows;
+  p.few = rows / E < 16;
+  p.gp.bm_big = p.few ? kFp8TileRows : 256;
+  p.gp.bm_small = 32;
   p.gp.split_rows = 0;
-  p.max_tiles = (int)(rows / kFp8TileRows + E + 1);
+  p.max_tiles = (int)(rows / p.gp.bm_big + E + 1) + kUnits;
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at_ = o;
@@ -871,7 +877,7 @@ Fp8Plan plan_fp8(long long rows, int E, int inter) {
   p.flags = take(256);
   p.sched = take((size_t)p.max_tiles * sizeof(MTile));
   p.sched_count = take(16);
-  p.h = take((size_t)rows * inter * 4);
+  p.h = take(p.few ? (size_t)rows * inter * 4 : 0);
   p.hq = take((size_t)rows * inter);
   p.hsc = take((size_t)rows * (inter / 128) * 4);
   p.total = o;
@@ -884,17 +890,24 @@ moe_status run_ffn_fp8(const moe_shape& s, const void* x, const float* xsc, cons
   uint32_t* flags = at<uint32_t>(ws, p.flags);
   MTile* sched = at<MTile>(ws, p.sched);
   int32_t* count = at<int32_t>(ws, p.sched_count);
-  float* h = at<float>(ws, p.h);
   uint8_t* hq = at<uint8_t>(ws, p.hq);
   float* hsc = at<float>(ws, p.hsc);
-  MOE_HIP(launch_build_schedule(offsets, E, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags));
-  const Fp8Args up{static_cast<const uint8_t*>(x), xsc, H / 128, 1, static_cast<const uint8_t*>(w.gate),
-                   static_cast<const uint8_t*>(w.up), w.gate_scales, w.up_scales, I, H, h, MOE_F32, sched, count, 0,
-                   flags};
+  MOE_HIP(launch_build_schedule(offsets, E, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags,
+                                p.few ? 0 : (H + 255) / 256));
+  Fp8Args up{static_cast<const uint8_t*>(x), xsc, H / 128, 1, static_cast<const uint8_t*>(w.gate),
+             static_cast<const uint8_t*>(w.up), w.gate_scales, w.up_scales, I, H, hq, MOE_F32, sched, count, 0,
+             flags, hsc, slots};
+  Fp8Args down{hq, hsc, 1, slots, static_cast<const uint8_t*>(w.down), nullptr, w.down_scales, nullptr, H, I,
+               y, y_dtype, sched, count, 0, flags, nullptr, 0};
+  if (p.few) {
+    up.out = at<float>(ws, p.h);
+    MOE_HIP(launch_gemm_fp8_few(up, true, p.max_tiles, st));
+    MOE_HIP(launch_quant_fp8(MOE_F32, up.out, slots, I, offsets + E, hq, hsc, st));
+    down.sa_row = I / 128, down.sa_group = 1;
+    MOE_HIP(launch_gemm_fp8_few(down, false, p.max_tiles, st));
+    return MOE_OK;
+  }
   MOE_HIP(launch_gemm_fp8(up, true, p.max_tiles, st));
-  MOE_HIP(launch_quant_fp8(MOE_F32, h, slots, I, offsets + E, hq, hsc, st));
-  const Fp8Args down{hq, hsc, I / 128, 1, static_cast<const uint8_t*>(w.down), nullptr, w.down_scales, nullptr, H, I,
-                     y, y_dtype, sched, count, 0, flags};
   MOE_HIP(launch_gemm_fp8(down, false, p.max_tiles, st));
   return MOE_OK;
 }
@@ -1701,12 +1714,13 @@ moe_status moe_grouped_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_
   MTile* sched = expert_offsets ? at<MTile>(ws, p.sched) : nullptr;
   int32_t* count = at<int32_t>(ws, p.sched_count);
   if (expert_offsets)
-    MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags));
+    MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags,
+                                  p.few ? 0 : (n + 255) / 256));
   else
     MOE_HIP(launch_clear_flags(flags, st));
   const Fp8Args g{static_cast<const uint8_t*>(a), a_scales, k / 128, 1, static_cast<const uint8_t*>(b), nullptr,
-                  b_scales, nullptr, n, k, y, y_dtype, sched, count, rows, flags};
-  MOE_HIP(launch_gemm_fp8(g, false, p.max_tiles, st));
+                  b_scales, nullptr, n, k, y, y_dtype, sched, count, rows, flags, nullptr, 0};
+  MOE_HIP(p.few ? launch_gemm_fp8_few(g, false, p.max_tiles, st) : launch_gemm_fp8(g, false, p.max_tiles, st));
   return MOE_OK;
 }
 

@@ -323,14 +323,19 @@ struct Fp8Args {
   const float* sb1;
   int N, K;
   void* out;
-  int y_dtype;            // MOE_F16 or MOE_BF16 (one matrix); fp32 h (gate/up)
-  const MTile* sched;     // row tiles of kFp8TileRows; null: rows [0, static_rows) of expert 0
+  int y_dtype;            // MOE_F16 or MOE_BF16 (one matrix)
+  const MTile* sched;     // row tiles; null: rows [0, static_rows) of expert 0
   const int32_t* count;
   int static_rows;
   uint32_t* flags;
+  float* out_scales;      // gate/up: scale of h row r, group g at g * out_group + r
+  long long out_group;
 };
-constexpr int kFp8TileRows = 64;
+// one matrix: y; dual (gate/up): h as codes and scales.  Row tiles of up to 256 rows.
 hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, int max_tiles, hipStream_t st);
+// few rows, tiles of kFp8TileRows; dual: fp32 h
+constexpr int kFp8TileRows = 64;
+hipError_t launch_gemm_fp8_few(const Fp8Args& a, bool dual, int max_tiles, hipStream_t st);
 
 // rows [rows][cols] (cols a multiple of 128) to codes and scales [rows][cols / 128];
 // rows at and beyond *rows_dev (nullable) are left alone

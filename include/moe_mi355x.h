@@ -506,8 +506,8 @@ moe_status moe_grouped_ffn_int8(const moe_shape* shape, const int8_t* x_codes, c
  *   y[r][n] = sum over blocks b of scale_a[r][b] * scale_b[n / 128][b] *
  *             sum over k in b of code_a[r][k] * code_b[n][k].
  * Row codes [rows][K], scales [rows][K / 128]; weight codes [E][N][K], scales
- * [E][ceil(N / 128)][K / 128].  K is a multiple of 128, N of 16 (the calls with a
- * shape: H and I multiples of 128, act_dtype MOE_BF16).
+ * [E][ceil(N / 128)][K / 128].  K is a multiple of 128 and at most 2^20, N a multiple
+ * of 16 (the calls with a shape: H and I multiples of 128, act_dtype MOE_BF16).
  * The matrix units add the products of a group of codes after aligning them to
  * the largest one, dropping what lies below about 2^-13 of it; the groups' sums
  * go on in fp32.  Sums of codes of rounded normal values are off by 1.4e-5 of
@@ -516,8 +516,9 @@ moe_status moe_grouped_ffn_int8(const moe_shape* shape, const int8_t* x_codes, c
  * MOE_F16 or MOE_BF16, MOE_F32 is MOE_ERR_UNSUPPORTED.
  * A block with an infinity or NaN gets unspecified codes and a scale that is not
  * finite (NaN for a NaN); a row of a product with such a scale, or with a NaN
- * code, is NaN, as is a column of such a weight block.  A scale of 0 may count as
- * the smallest positive number. */
+ * code, is NaN, as is a column of such a weight block.  A scale
+ * below fp32's normal range (2^-126; 0 among them) may count as any number up to
+ * that. */
 
 /* Quantises rows src [rows][cols] (MOE_BF16, MOE_F32 or MOE_F16; cols a multiple
  * of 128). */
