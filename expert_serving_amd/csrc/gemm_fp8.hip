@@ -74,10 +74,13 @@ __device__ __forceinline__ bool xcd_index(int real, int& L) {
   return L < real;
 }
 
-// scale 2^e m: m in [1, 2) with the scale's sign, and e as the exponent byte in the
-// word's top byte (a scale below fp32's normal range counts as 2^-127 m)
-__device__ __forceinline__ float scale_m(uint32_t w) { return __uint_as_float((w & 0x807FFFFFu) | 0x3F800000u); }
+// A scale 2^e m with m in [1, 2): the word with its exponent in the top byte, which the
+// MFMA takes as E8M0 (a scale below fp32's normal range counts as 2^-127 m), and m
 __device__ __forceinline__ int scale_e(uint32_t w) { return (int)(w << 1); }
+__device__ __forceinline__ float unit_of(int e) { return __uint_as_float((((uint32_t)e >> 1) & 0x007FFFFFu) | 0x3F800000u); }
+__device__ __forceinline__ f32x16 mfma_scaled(i32x8 w, i32x8 x, f32x16 c, int ew, int ex) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 0, 0, 3, ew, 3, ex);
+}
 
 constexpr int tile_lds(int BM, int BN) {
   return 2 * (BM + BN) * kStage + 2 * kChunkStages * (BM + 64) * 4;
@@ -167,35 +170,34 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[f][b][q] = 0.f;
   i32x8 xa[FM], wf[2][FN];
-  float mt[FM], mw[FN], rt[FM], rw[FN];  // units of the sums, their change at the next stage
+  // exponent words of the current stage's scales, and the change of the sums' units
+  // that its first step makes
   int et[FM], ew[FN];
-  uint32_t nt[FM], nw[FN];               // scale words of the next stage
-  auto read_scales = [&](int s) {
+  float rt[FM], rw[FN];
+  auto read_scales = [&](int s, uint32_t (&nt)[FM], uint32_t (&nw)[FN]) {
     const int at = ((s / kChunkStages) & 1) * kChunkStages + s % kChunkStages;
 #pragma unroll
     for (int b = 0; b < FM; ++b) nt[b] = __float_as_uint(s_row[at * BM + wm * WM + b * 32 + fr]);
 #pragma unroll
     for (int f = 0; f < FN; ++f) nw[f] = __float_as_uint(s_wgt[at * 64 + (DUAL ? f : (wn * WN) / kFp8Block)]);
   };
-  auto next_units = [&]() {
+  auto next_units = [&](const uint32_t (&nt)[FM], const uint32_t (&nw)[FN]) {
 #pragma unroll
     for (int b = 0; b < FM; ++b) {
-      const float m = scale_m(nt[b]);
-      rt[b] = mt[b] * __builtin_amdgcn_rcpf(m);
-      mt[b] = m;
+      rt[b] = unit_of(et[b]) * __builtin_amdgcn_rcpf(unit_of(scale_e(nt[b])));
+      et[b] = scale_e(nt[b]);
     }
 #pragma unroll
     for (int f = 0; f < FN; ++f) {
-      const float m = scale_m(nw[f]);
-      rw[f] = mw[f] * __builtin_amdgcn_rcpf(m);
-      mw[f] = m;
+      rw[f] = unit_of(ew[f]) * __builtin_amdgcn_rcpf(unit_of(scale_e(nw[f])));
+      ew[f] = scale_e(nw[f]);
     }
   };
 
 #pragma unroll
-  for (int b = 0; b < FM; ++b) mt[b] = 1.f;
+  for (int b = 0; b < FM; ++b) et[b] = 0;
 #pragma unroll
-  for (int f = 0; f < FN; ++f) mw[f] = 1.f;
+  for (int f = 0; f < FN; ++f) ew[f] = 0;
   load_scales(0);
 #pragma unroll
   for (int i = 0; i < NI; ++i) load(0, 0, i);
@@ -203,23 +205,23 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
   for (int i = 0; i < NI; ++i) load(1, min(1, S - 1), i);
   __builtin_amdgcn_s_waitcnt(0);
   raw_barrier();
-  read_scales(0);
+  {
+    uint32_t nt[FM], nw[FN];
+    read_scales(0, nt, nw);
+    next_units(nt, nw);
+  }
 #pragma unroll
   for (int f = 0; f < FN; ++f) wf[0][f] = frag_b(0, 0, f);
 #pragma unroll
   for (int b = 0; b < FM; ++b) xa[b] = frag_a(0, 0, b);
-  next_units();
 
   // no branch inside a stage: loads past the last one read it again, into the buffer
   // that is not read any more
   for (int c = 0; c < S; c += kChunkStages) {
     load_scales(c / kChunkStages + 1);
     for (int s = c; s < min(c + kChunkStages, S); ++s) {
-      // first step: the sums to this stage's units
-#pragma unroll
-      for (int b = 0; b < FM; ++b) et[b] = scale_e(nt[b]);
-#pragma unroll
-      for (int f = 0; f < FN; ++f) ew[f] = scale_e(nw[f]);
+      // first step: the sums to this stage's units, the multiplications of one fragment
+      // beside the MFMA of the one before
 #pragma unroll
       for (int f = 0; f < FN; ++f) wf[1][f] = frag_b(s, 1, f);
 #pragma unroll
@@ -229,30 +231,32 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
           const float r = rt[b] * rw[f];
 #pragma unroll
           for (int q = 0; q < 16; ++q) acc[f][b][q] *= r;
-          acc[f][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[0][f], xa[b], acc[f][b], 0, 0, 3, ew[f], 3, et[b]);
+          acc[f][b] = mfma_scaled(wf[0][f], xa[b], acc[f][b], ew[f], et[b]);
+          __builtin_amdgcn_sched_barrier(0);
         }
         xa[b] = frag_a(s, 1, b);
-        __builtin_amdgcn_sched_barrier(0);
       }
       // every wavefront has this buffer's last fragments, and its loads of the next
       // stage have landed
       __builtin_amdgcn_s_waitcnt(0);
       raw_barrier();
       __builtin_amdgcn_sched_barrier(0);
-      read_scales(min(s + 1, S - 1));
+      uint32_t nt[FM], nw[FN];
+      read_scales(min(s + 1, S - 1), nt, nw);
 #pragma unroll
       for (int f = 0; f < FN; ++f) wf[0][f] = frag_b(s + 1, 0, f);
 #pragma unroll
       for (int b = 0; b < FM; ++b) {
 #pragma unroll
-        for (int f = 0; f < FN; ++f)
-          acc[f][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[1][f], xa[b], acc[f][b], 0, 0, 3, ew[f], 3, et[b]);
+        for (int f = 0; f < FN; ++f) {
+          acc[f][b] = mfma_scaled(wf[1][f], xa[b], acc[f][b], ew[f], et[b]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
         xa[b] = frag_a(s + 1, 0, b);
 #pragma unroll
         for (int i = b * NI / FM; i < (b + 1) * NI / FM; ++i) load(s & 1, min(s + 2, S - 1), i);
-        __builtin_amdgcn_sched_barrier(0);
       }
-      next_units();
+      next_units(nt, nw);
     }
   }
   __builtin_amdgcn_s_waitcnt(0);
@@ -269,7 +273,7 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
 #pragma unroll
     for (int b = 0; b < FM; ++b) {
       uint32_t top = 0u;
-      const float u0 = mt[b] * mw[0], u1 = mt[b] * mw[1];
+      const float u0 = unit_of(et[b]) * unit_of(ew[0]), u1 = unit_of(et[b]) * unit_of(ew[1]);
       const bool in = n0 + wn * WN < N;   // (N is a multiple of 128)
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
@@ -310,7 +314,7 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
       const bool real = wm * WM + b * 32 + fr < rows;
 #pragma unroll
       for (int f = 0; f < FN; ++f) {
-        const float u = mt[b] * mw[f];
+        const float u = unit_of(et[b]) * unit_of(ew[f]);
 #pragma unroll
         for (int qi = 0; qi < 4; ++qi) {
           const bool in = n0 + wn * WC + f * 32 + 8 * qi < N;
