@@ -26,7 +26,7 @@ ARCH = "gfx950"
 
 SOURCES = ["moe_api.hip", "router.hip", "route.hip", "dispatch.hip", "gemm.hip", "combine.hip",
            "mxfp8.hip", "ep.hip", "int8.hip", "stream_i8.hip", "block.hip", "route_biased.hip",
-           "rows.hip", "gemm_fp8.hip"]
+           "rows.hip", "gemm_fp8.hip", "stream_fp8.hip"]
 PEAKS_SRC = "peaks.hip"
 PEAKS_BIN = os.path.join(HERE, "moe_peaks")
 NO_CONTRACT = {"route.hip"}

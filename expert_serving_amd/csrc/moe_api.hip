@@ -855,19 +855,25 @@ moe_status check_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t E) {
 
 struct Fp8Plan {
   GemmPlan gp;
-  bool few;
-  int max_tiles;
+  bool stream;
+  int max_tiles;  // row tiles, of the stream's height where it is one
   size_t flags, sched, sched_count, h, hq, hsc, total;
 };
 
-// rows over E experts; inter > 0: an FFN's h of that many columns
-Fp8Plan plan_fp8(long long rows, int E, int inter) {
+// Products of fewer than 64 rows per expert stream their weights while the 32-row tiles
+// together read at most 240 MB, and at most 120 KB per k of their (mean) K.
+bool stream_fp8(const moe_shape& s, long long matrix_bytes, long long mean_k) { return stream_i8(s, matrix_bytes, mean_k); }
+
+// a batch of one slot per row of n columns and K = k, or (inter > 0) the FFN of a shape
+Fp8Plan plan_fp8(const moe_shape& s, bool ffn) {
   Fp8Plan p{};
-  p.few = rows / E < 16;
-  p.gp.bm_big = p.few ? kFp8TileRows : 256;
+  const long long rows = (long long)s.num_tokens * s.top_k, H = s.hidden, I = s.intermediate;
+  const int E = s.num_experts;
+  p.stream = rows > 0 && (ffn ? stream_fp8(s, 3 * H * I, (2 * H + I) / 3) : stream_fp8(s, H * I, I));
+  p.gp.bm_big = 256;
   p.gp.bm_small = 32;
   p.gp.split_rows = 0;
-  p.max_tiles = (int)(rows / p.gp.bm_big + E + 1) + kUnits;
+  p.max_tiles = p.stream ? (int)stream_tiles(s) : (int)(rows / 256 + E + 1) + kUnits;  // (cut tiles)
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at_ = o;
@@ -875,13 +881,26 @@ Fp8Plan plan_fp8(long long rows, int E, int inter) {
     return at_;
   };
   p.flags = take(256);
-  p.sched = take((size_t)p.max_tiles * sizeof(MTile));
+  p.sched = take(p.stream ? 0 : (size_t)p.max_tiles * sizeof(MTile));
   p.sched_count = take(16);
-  p.h = take(p.few ? (size_t)rows * inter * 4 : 0);
-  p.hq = take((size_t)rows * inter);
-  p.hsc = take((size_t)rows * (inter / 128) * 4);
+  if (ffn) {
+    p.h = take(p.stream ? (size_t)rows * I * 4 : 0);
+    p.hq = take((size_t)rows * I);
+    p.hsc = take((size_t)rows * (I / 128) * 4);
+  }
   p.total = o;
   return p;
+}
+
+// one product, planned as the down projection of a layer with one slot per row
+Fp8Plan plan_gemm_fp8(int rows, int n, int k, int E, moe_shape& s) {
+  s = moe_shape{};
+  s.num_tokens = rows;
+  s.hidden = n;
+  s.intermediate = k;
+  s.num_experts = E;
+  s.top_k = 1;
+  return plan_fp8(s, false);
 }
 
 moe_status run_ffn_fp8(const moe_shape& s, const void* x, const float* xsc, const int32_t* offsets,
@@ -892,21 +911,26 @@ moe_status run_ffn_fp8(const moe_shape& s, const void* x, const float* xsc, cons
   int32_t* count = at<int32_t>(ws, p.sched_count);
   uint8_t* hq = at<uint8_t>(ws, p.hq);
   float* hsc = at<float>(ws, p.hsc);
-  MOE_HIP(launch_build_schedule(offsets, E, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags,
-                                p.few ? 0 : (H + 255) / 256));
   Fp8Args up{static_cast<const uint8_t*>(x), xsc, H / 128, 1, static_cast<const uint8_t*>(w.gate),
              static_cast<const uint8_t*>(w.up), w.gate_scales, w.up_scales, I, H, hq, MOE_F32, sched, count, 0,
-             flags, hsc, slots};
+             flags, hsc, slots, offsets};
   Fp8Args down{hq, hsc, 1, slots, static_cast<const uint8_t*>(w.down), nullptr, w.down_scales, nullptr, H, I,
-               y, y_dtype, sched, count, 0, flags, nullptr, 0};
-  if (p.few) {
-    up.out = at<float>(ws, p.h);
-    MOE_HIP(launch_gemm_fp8_few(up, true, p.max_tiles, st));
-    MOE_HIP(launch_quant_fp8(MOE_F32, up.out, slots, I, offsets + E, hq, hsc, st));
-    down.sa_row = I / 128, down.sa_group = 1;
-    MOE_HIP(launch_gemm_fp8_few(down, false, p.max_tiles, st));
+               y, y_dtype, sched, count, 0, flags, nullptr, 0, offsets};
+  if (p.stream) {
+    float* h = at<float>(ws, p.h);
+    up.out = h;
+    MOE_HIP(launch_stream_fp8(up, true, false, E, p.max_tiles, slots, true, st));
+    const bool fused = stream_quantises(slots, I);
+    if (fused) {
+      down.A = reinterpret_cast<const uint8_t*>(h);
+    } else {
+      MOE_HIP(launch_quant_fp8(MOE_F32, h, slots, I, offsets + E, hq, hsc, st, flags));
+      down.sa_row = I / 128, down.sa_group = 1;
+    }
+    MOE_HIP(launch_stream_fp8(down, false, fused, E, p.max_tiles, slots, false, st));
     return MOE_OK;
   }
+  MOE_HIP(launch_build_schedule(offsets, E, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags, (H + 255) / 256));
   MOE_HIP(launch_gemm_fp8(up, true, p.max_tiles, st));
   MOE_HIP(launch_gemm_fp8(down, false, p.max_tiles, st));
   return MOE_OK;
@@ -1688,7 +1712,8 @@ moe_status moe_quantize_fp8_weights(int32_t num_experts, int32_t n, int32_t k, i
 moe_status moe_workspace_size_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_experts, size_t* bytes) {
   MOE_TRY(check_gemm_fp8(rows, n, k, num_experts));
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  *bytes = plan_fp8(rows, num_experts, 0).total;
+  moe_shape s;
+  *bytes = plan_gemm_fp8(rows, n, k, num_experts, s).total;
   return MOE_OK;
 }
 
@@ -1706,28 +1731,35 @@ moe_status moe_grouped_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_
   MOE_TRY(need4(b_scales));
   MOE_TRY(need(y));
   MOE_TRY(need(ws));
-  const Fp8Plan p = plan_fp8(rows, num_experts, 0);
+  moe_shape s;
+  const Fp8Plan p = plan_gemm_fp8(rows, n, k, num_experts, s);
   if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
   if (rows == 0) return MOE_OK;
   hipStream_t st = static_cast<hipStream_t>(stream);
   uint32_t* flags = at<uint32_t>(ws, p.flags);
   MTile* sched = expert_offsets ? at<MTile>(ws, p.sched) : nullptr;
   int32_t* count = at<int32_t>(ws, p.sched_count);
+  const Fp8Args g{static_cast<const uint8_t*>(a), a_scales, k / 128, 1, static_cast<const uint8_t*>(b), nullptr,
+                  b_scales, nullptr, n, k, y, y_dtype, sched, count, rows, flags, nullptr, 0, expert_offsets};
+  if (p.stream) {
+    // (an fp16 y adds to the flag word, which then has to be clear before)
+    if (y_dtype == MOE_F16) MOE_HIP(launch_clear_flags(flags, st));
+    MOE_HIP(launch_stream_fp8(g, false, false, num_experts, p.max_tiles, rows, y_dtype != MOE_F16, st));
+    return MOE_OK;
+  }
   if (expert_offsets)
     MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags,
-                                  p.few ? 0 : (n + 255) / 256));
+                                  (n + 255) / 256));
   else
     MOE_HIP(launch_clear_flags(flags, st));
-  const Fp8Args g{static_cast<const uint8_t*>(a), a_scales, k / 128, 1, static_cast<const uint8_t*>(b), nullptr,
-                  b_scales, nullptr, n, k, y, y_dtype, sched, count, rows, flags, nullptr, 0};
-  MOE_HIP(p.few ? launch_gemm_fp8_few(g, false, p.max_tiles, st) : launch_gemm_fp8(g, false, p.max_tiles, st));
+  MOE_HIP(launch_gemm_fp8(g, false, p.max_tiles, st));
   return MOE_OK;
 }
 
 moe_status moe_workspace_size_fp8(const moe_shape* shape, size_t* bytes) {
   MOE_TRY(check_fp8_shape(shape));
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  *bytes = plan_fp8((long long)shape->num_tokens * shape->top_k, shape->num_experts, shape->intermediate).total;
+  *bytes = plan_fp8(*shape, true).total;
   return MOE_OK;
 }
 
@@ -1743,7 +1775,7 @@ moe_status moe_grouped_ffn_fp8(const moe_shape* shape, const void* x_codes, cons
   MOE_TRY(check_fp8_ffn(experts));
   MOE_TRY(need(y_perm));
   MOE_TRY(need(ws));
-  const Fp8Plan p = plan_fp8((long long)s.num_tokens * s.top_k, s.num_experts, s.intermediate);
+  const Fp8Plan p = plan_fp8(s, true);
   if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
   if (s.num_tokens == 0) return MOE_OK;
   return run_ffn_fp8(s, x_codes, x_scales, expert_offsets, *experts, y_dtype, y_perm, ws, p,

@@ -330,17 +330,23 @@ struct Fp8Args {
   uint32_t* flags;
   float* out_scales;      // gate/up: scale of h row r, group g at g * out_group + r
   long long out_group;
+  const int32_t* offsets; // streams: [E + 1]; null: rows [0, static_rows) of expert 0
 };
 // one matrix: y; dual (gate/up): h as codes and scales.  Row tiles of up to 256 rows.
 hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, int max_tiles, hipStream_t st);
-// few rows, tiles of kFp8TileRows; dual: fp32 h
-constexpr int kFp8TileRows = 64;
-hipError_t launch_gemm_fp8_few(const Fp8Args& a, bool dual, int max_tiles, hipStream_t st);
+// The products of few rows (stream_fp8.hip), 32-row tiles; max_tiles bounds them,
+// max_rows the rows of an expert.  dual: fp32 h.  quantise (one matrix, max_rows <= 16):
+// A holds fp32 h, quantised on the way (an h that is not finite sets MOE_FLAG_H_RANGE).
+// clear_flags: the launch first clears the flag word (it adds to it only for an fp16 y or
+// where it quantises, so then another launch has to clear it).
+hipError_t launch_stream_fp8(const Fp8Args& a, bool dual, bool quantise, int E, int max_tiles, int max_rows,
+                             bool clear_flags, hipStream_t st);
 
 // rows [rows][cols] (cols a multiple of 128) to codes and scales [rows][cols / 128];
-// rows at and beyond *rows_dev (nullable) are left alone
+// rows at and beyond *rows_dev (nullable) are left alone.  h_flags (nullable): a value
+// that is not finite sets MOE_FLAG_H_RANGE
 hipError_t launch_quant_fp8(int src_dtype, const void* src, int rows, int cols, const int32_t* rows_dev, void* codes,
-                            float* scales, hipStream_t st);
+                            float* scales, hipStream_t st, uint32_t* h_flags = nullptr);
 hipError_t launch_quant_fp8_weights(int src_dtype, const void* src, int experts, int n, int k, void* codes,
                                     float* scales, hipStream_t st);
 

@@ -42,6 +42,29 @@ __device__ __forceinline__ float f8_quotient(float v, const F8Block& b) {
   return fminf(fmaxf(fmaf(rest, b.rcp, q0), -kFp8Max), kFp8Max);
 }
 
+// The same for values that carry roundings of their own (h of an FFN), where the last
+// bit of the quotient decides nothing that they do not: one product.
+struct F8Near {
+  float pre, factor;  // 448 / (amax * pre); 0 for a block of zeros
+};
+__device__ __forceinline__ F8Near f8_near(float amax) {
+  F8Near r;
+  r.pre = amax < 1e-20f ? 0x1p60f : 1.0f;
+  const float x = amax * r.pre;
+  r.factor = x > 0.f ? kFp8Max * __builtin_amdgcn_rcpf(x) : 0.f;
+  return r;
+}
+__device__ __forceinline__ float f8_code(float v, const F8Near& b) {
+  return __builtin_amdgcn_fmed3f((v * b.pre) * b.factor, -kFp8Max, kFp8Max);
+}
+
+// A scale 2^e m with m in [1, 2): the word with its exponent in the top byte, which the
+// matrix units take as E8M0 (a scale below fp32's normal range counts as 2^-127 m), and
+// m, from the scale's word or from that one.
+__device__ __forceinline__ int f8_exponent(uint32_t scale) { return (int)(scale << 1); }
+__device__ __forceinline__ float f8_unit(uint32_t scale) { return __uint_as_float((scale & 0x007FFFFFu) | 0x3F800000u); }
+__device__ __forceinline__ float f8_unit_of(int e) { return f8_unit((uint32_t)e >> 1); }
+
 // four quotients to four E4M3 bytes, nearest, ties to even
 __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d) {
   int p = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);

@@ -196,14 +196,17 @@ __global__ __launch_bounds__(256) void k_dispatch_rows_fp8(int items, int H, int
 template <int DT>
 __global__ __launch_bounds__(256) void k_quant_fp8(long long items, int per_row, const int32_t* __restrict__ rows_dev,
                                                    const void* __restrict__ src, uint8_t* __restrict__ codes,
-                                                   float* __restrict__ scales) {
+                                                   float* __restrict__ scales, uint32_t* __restrict__ h_flags) {
   const long long step = (long long)gridDim.x * 256;
   if (rows_dev) items = min(items, (long long)*rows_dev * per_row);
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < items; i += step) {
     u32x4 w;
     const float scale = quantise16<DT>(src, (size_t)i, w);
     *reinterpret_cast<u32x4*>(codes + 16 * i) = w;
-    if ((i & 7) == 0) scales[i >> 3] = scale;
+    if ((i & 7) == 0) {
+      scales[i >> 3] = scale;
+      if (h_flags && !(scale <= 3.402823466e38f)) atomicOr(h_flags, (uint32_t)MOE_FLAG_H_RANGE);
+    }
   }
 }
 
@@ -406,12 +409,12 @@ hipError_t launch_dispatch_rows_fp8(const moe_shape& s, int dtype, const void* x
 }
 
 hipError_t launch_quant_fp8(int src_dtype, const void* src, int rows, int cols, const int32_t* rows_dev, void* codes,
-                            float* scales, hipStream_t st) {
+                            float* scales, hipStream_t st, uint32_t* h_flags) {
   const long long items = (long long)rows * (cols / 16), blocks = (items + 255) / 256;
   if (items <= 0) return hipSuccess;
   return with_type(src_dtype, [&](auto dt) {
     hipLaunchKernelGGL(k_quant_fp8<dt.value>, dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(256), 0, st,
-                       items, cols / 16, rows_dev, src, static_cast<uint8_t*>(codes), scales);
+                       items, cols / 16, rows_dev, src, static_cast<uint8_t*>(codes), scales, h_flags);
     return hipGetLastError();
   });
 }
