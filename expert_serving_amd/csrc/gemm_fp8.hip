@@ -16,7 +16,7 @@
 // One block of 8 wavefronts (two per SIMD) makes a tile of up to 256 token rows (in
 // steps of 64) x 256 weight rows (gate/up: 128 of each matrix), weights as the MFMA's
 // first operand, so that a lane's 16 sums of a fragment belong to one token row.  A
-// stage is K = 128 in one of two LDS buffers: rows of 128 bytes, 16-byte chunk c of
+// stage is K = 128 in one of two (for low tiles three) LDS buffers: rows of 128 bytes, 16-byte chunk c of
 // row r at c ^ ((r >> 1) & 7), filled straight from memory (8 rows x 128 bytes per
 // wavefront load).  A stage has two steps of K = 64.  In the first the fragments of
 // the second are read, which is the last use of the buffer; a barrier; in the second
@@ -60,6 +60,13 @@ __device__ __forceinline__ void raw_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// s_waitcnt for this wavefront's LDS reads, and for all but its last N loads
+template <int N>
+__device__ __forceinline__ void wait_lds_and_loads() {
+  static_assert(N < 64, "vmcnt");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));
+}
+
 // Logical index of this block among `real` tiles, XCD by XCD (block b runs on XCD
 // b % 8), so that every XCD gets a contiguous range; false behind the last.
 __device__ __forceinline__ bool xcd_index(int real, int& L) {
@@ -75,9 +82,15 @@ __device__ __forceinline__ f32x16 mfma_scaled(i32x8 w, i32x8 x, f32x16 c, int ew
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 0, 0, 3, ew, 3, ex);
 }
 
+// LDS buffers of a tile: as many as fit beside the scales (half a compute unit's LDS for
+// BN 128).  The few rows of a low tile stream their weights, and what is under way
+// decides how fast.
+constexpr int tile_stages(int BM, int BN) { return BN == 128 ? (BM <= 64 ? 3 : 2) : (BM <= 128 ? 3 : 2); }
 constexpr int tile_lds(int BM, int BN) {
-  return 2 * (BM + BN) * kStage + 2 * kChunkStages * (BM + 64) * 4;
+  return tile_stages(BM, BN) * (BM + BN) * kStage + 2 * kChunkStages * (BM + 64) * 4;
 }
+
+constexpr int max_of(int a, int b) { return a > b ? a : b; }
 
 // BM token rows x BN weight rows (DUAL: BN / 2 of each matrix).
 template <int BM, int BN, bool DUAL>
@@ -85,7 +98,7 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
   constexpr int FM = BM / 64, FN = BN / 128;   // fragments of a wavefront: 2 x 4 wavefronts
   constexpr int WM = BM / 2, WN = DUAL ? BN / 8 : BN / 4;  // its rows and columns (of each matrix)
   constexpr int NI = FM + BN / 64;             // 8-row loads per wavefront and stage
-  constexpr int BUF = (BM + BN) * kStage;
+  constexpr int BUF = (BM + BN) * kStage, NS = tile_stages(BM, BN);
   constexpr int COLS = DUAL ? BN / 2 : BN;     // output columns
   static_assert(!DUAL || BN == 256, "a block of h columns per tile");
   const int N = a.N, K = a.K, S = K / kStage;
@@ -126,7 +139,7 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
   };
   // the scales of stages 8 c .. 8 c + 7: wavefront w those of stage 8 c + w, BM token
   // rows, then the weight blocks of the tile (two, in turn over the lanes)
-  float* const s_row = reinterpret_cast<float*>(smem + 2 * BUF);  // [2][8][BM]
+  float* const s_row = reinterpret_cast<float*>(smem + NS * BUF);  // [2][8][BM]
   float* const s_wgt = s_row + 2 * kChunkStages * BM;             // [2][8][64]
   const int nblocks = (N + kFp8Block - 1) / kFp8Block;
   const float* const swl = (DUAL && (lane & 1) ? a.sb1 : a.sb0) +
@@ -152,8 +165,8 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
     return cat8(*reinterpret_cast<const u32x4*>(row + (((4 * h + fk) ^ swz) << 4)),
                 *reinterpret_cast<const u32x4*>(row + (((4 * h + 2 + fk) ^ swz) << 4)));
   };
-  auto frag_a = [&](int s, int h, int b) { return frag(fa + (s & 1) * BUF + b * 32 * kStage, h); };
-  auto frag_b = [&](int s, int h, int f) { return frag(fb + (s & 1) * BUF + f * (DUAL ? COLS : 32) * kStage, h); };
+  auto frag_a = [&](int buf, int h, int b) { return frag(fa + buf * BUF + b * 32 * kStage, h); };
+  auto frag_b = [&](int buf, int h, int f) { return frag(fb + buf * BUF + f * (DUAL ? COLS : 32) * kStage, h); };
 
   f32x16 acc[FN][FM];
 #pragma unroll
@@ -193,10 +206,10 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
   for (int f = 0; f < FN; ++f) ew[f] = 0;
   load_scales(0);
 #pragma unroll
-  for (int i = 0; i < NI; ++i) load(0, 0, i);
+  for (int s = 0; s < NS; ++s)
 #pragma unroll
-  for (int i = 0; i < NI; ++i) load(1, min(1, S - 1), i);
-  __builtin_amdgcn_s_waitcnt(0);
+    for (int i = 0; i < NI; ++i) load(s, min(s, S - 1), i);
+  wait_lds_and_loads<NI * (NS - 1)>();
   raw_barrier();
   {
     uint32_t nt[FM], nw[FN];
@@ -210,13 +223,15 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
 
   // no branch inside a stage: loads past the last one read it again, into the buffer
   // that is not read any more
+  int cur = 0;  // buffer of stage s
   for (int c = 0; c < S; c += kChunkStages) {
     load_scales(c / kChunkStages + 1);
     for (int s = c; s < min(c + kChunkStages, S); ++s) {
+      const int after = cur + 1 == NS ? 0 : cur + 1;
       // first step: the sums to this stage's units, the multiplications of one fragment
       // beside the MFMA of the one before
 #pragma unroll
-      for (int f = 0; f < FN; ++f) wf[1][f] = frag_b(s, 1, f);
+      for (int f = 0; f < FN; ++f) wf[1][f] = frag_b(cur, 1, f);
 #pragma unroll
       for (int b = 0; b < FM; ++b) {
 #pragma unroll
@@ -227,17 +242,18 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
           acc[f][b] = mfma_scaled(wf[0][f], xa[b], acc[f][b], ew[f], et[b]);
           __builtin_amdgcn_sched_barrier(0);
         }
-        xa[b] = frag_a(s, 1, b);
+        xa[b] = frag_a(cur, 1, b);
       }
       // every wavefront has this buffer's last fragments, and its loads of the next
-      // stage have landed
-      __builtin_amdgcn_s_waitcnt(0);
+      // stage have landed (those of later ones may be under way; a chunk's scales among
+      // them only make the wait longer)
+      wait_lds_and_loads<NI * (NS - 2)>();
       raw_barrier();
       __builtin_amdgcn_sched_barrier(0);
       uint32_t nt[FM], nw[FN];
       read_scales(min(s + 1, S - 1), nt, nw);
 #pragma unroll
-      for (int f = 0; f < FN; ++f) wf[0][f] = frag_b(s + 1, 0, f);
+      for (int f = 0; f < FN; ++f) wf[0][f] = frag_b(after, 0, f);
 #pragma unroll
       for (int b = 0; b < FM; ++b) {
 #pragma unroll
@@ -245,11 +261,12 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
           acc[f][b] = mfma_scaled(wf[1][f], xa[b], acc[f][b], ew[f], et[b]);
           __builtin_amdgcn_sched_barrier(0);
         }
-        xa[b] = frag_a(s + 1, 0, b);
+        xa[b] = frag_a(after, 0, b);
 #pragma unroll
-        for (int i = b * NI / FM; i < (b + 1) * NI / FM; ++i) load(s & 1, min(s + 2, S - 1), i);
+        for (int i = b * NI / FM; i < (b + 1) * NI / FM; ++i) load(cur, min(s + NS, S - 1), i);
       }
       next_units(nt, nw);
+      cur = after;
     }
   }
   __builtin_amdgcn_s_waitcnt(0);
@@ -344,14 +361,16 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
 
 // Row tiles of up to 256 rows, each at the height its rows need; the blocks of an
 // expert's neighbouring row tiles come column by column (see the int8 form of the
-// same order).
+// same order).  BN 128: a row tile is taken as two of up to 128; such blocks fit a
+// compute unit twice.
 template <int BN, bool DUAL>
-__global__ __launch_bounds__(512) void k_gemm_fp8(const Fp8Args a, int mslots, int ntiles) {
+__global__ __launch_bounds__(512, BN == 128 ? 4 : 2) void k_gemm_fp8(const Fp8Args a, int mslots, int ntiles) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  const int mtiles = a.sched ? min(*a.count, mslots) : mslots;
+  constexpr bool HALVES = BN == 128;
+  const int mtiles = a.sched ? min(*a.count, mslots) : mslots, cols = ntiles * (HALVES ? 2 : 1);
   int L;
-  if (!xcd_index(mtiles * ntiles, L)) return;
-  const int at = L / ntiles;
+  if (!xcd_index(mtiles * cols, L)) return;
+  const int at = L / cols;
   int first, size;
   if (a.sched) {
     const int group = a.sched[at].group;
@@ -359,38 +378,50 @@ __global__ __launch_bounds__(512) void k_gemm_fp8(const Fp8Args a, int mslots, i
   } else {
     first = at / kTileGroup * kTileGroup, size = min(kTileGroup, mtiles - first);
   }
-  const int r = L - first * ntiles, col = r / size, i = first + (r - col * size);
+  const int r = L - first * cols, col = r / size, i = first + (r - col * size);
   MTile t;
   if (a.sched) t = a.sched[i];
   else t = MTile{0, 256 * i, min(256, a.static_rows - 256 * i), 0};
+  int ni = col;
+  if constexpr (HALVES) {
+    ni = col >> 1;
+    t.row0 += 128 * (col & 1);
+    t.rows = min(t.rows - 128 * (col & 1), 128);
+  }
   if (t.rows <= 0) return;
-  if (t.rows <= 64) tile_fp8<64, BN, DUAL>(smem, a, t, col);
-  else if (t.rows <= 128) tile_fp8<128, BN, DUAL>(smem, a, t, col);
-  else if (t.rows <= 192) tile_fp8<192, BN, DUAL>(smem, a, t, col);
-  else tile_fp8<256, BN, DUAL>(smem, a, t, col);
+  if (t.rows <= 64) {
+    tile_fp8<64, BN, DUAL>(smem, a, t, ni);
+  } else if (HALVES || t.rows <= 128) {
+    tile_fp8<128, BN, DUAL>(smem, a, t, ni);
+  } else if constexpr (!HALVES) {
+    if (t.rows <= 192) tile_fp8<192, BN, DUAL>(smem, a, t, ni);
+    else tile_fp8<256, BN, DUAL>(smem, a, t, ni);
+  }
 }
 
 template <int BN, bool DUAL>
 hipError_t launch_tiles(const Fp8Args& a, int max_tiles, hipStream_t st) {
   const int mslots = a.sched ? max_tiles : (a.static_rows + 255) / 256;
   if (mslots <= 0) return hipSuccess;
-  constexpr int lds = tile_lds(256, BN);
-  static_assert(lds <= 160 * 1024, "LDS");
+  constexpr int lds = BN == 128 ? max_of(tile_lds(64, BN), tile_lds(128, BN))
+                                : max_of(tile_lds(128, BN), tile_lds(256, BN));  // (64 and 192 rows take less)
+  static_assert(lds <= 160 * 1024 / (BN == 128 ? 2 : 1), "LDS");
   static std::atomic<uint64_t> set_on{0};
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(&k_gemm_fp8<BN, DUAL>), lds, set_on);
   if (e != hipSuccess) return e;
   constexpr int cols = DUAL ? BN / 2 : BN;
   const int ntiles = (a.N + cols - 1) / cols;
-  const long long grid = ((long long)mslots * ntiles + 7) / 8 * 8;
-  if (grid > 0x7fffff) return hipErrorInvalidValue;
+  const long long grid = ((long long)mslots * ntiles * (BN == 128 ? 2 : 1) + 7) / 8 * 8;
+  if (grid > 0x7fffff) return hipErrorInvalidValue;  // (2^32 threads of one axis)
   hipLaunchKernelGGL((k_gemm_fp8<BN, DUAL>), dim3((unsigned)grid), dim3(512), lds, st, a, mslots, ntiles);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, int max_tiles, hipStream_t st) {
-  return dual ? launch_tiles<256, true>(a, max_tiles, st) : launch_tiles<256, false>(a, max_tiles, st);
+hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, bool halves, int max_tiles, hipStream_t st) {
+  if (dual) return launch_tiles<256, true>(a, max_tiles, st);
+  return halves ? launch_tiles<128, false>(a, max_tiles, st) : launch_tiles<256, false>(a, max_tiles, st);
 }
 
 }  // namespace moe

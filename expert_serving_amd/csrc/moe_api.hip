@@ -864,6 +864,12 @@ struct Fp8Plan {
 // together read at most 240 MB, and at most 120 KB per k of their (mean) K.
 bool stream_fp8(const moe_shape& s, long long matrix_bytes, long long mean_k) { return stream_i8(s, matrix_bytes, mean_k); }
 
+bool few_tiles_fp8(const moe_shape& s, int n) {
+  const long long slots = (long long)s.num_tokens * s.top_k, E = s.num_experts;
+  const long long tiles = std::max(slots / 256 + (E + 1) / 2, std::min(slots, E));
+  return tiles * ((n + 255) / 256) < kComputeUnits * 2 / 3;
+}
+
 // a batch of one slot per row of n columns and K = k, or (inter > 0) the FFN of a shape
 Fp8Plan plan_fp8(const moe_shape& s, bool ffn) {
   Fp8Plan p{};
@@ -930,9 +936,11 @@ moe_status run_ffn_fp8(const moe_shape& s, const void* x, const float* xsc, cons
     MOE_HIP(launch_stream_fp8(down, false, fused, E, p.max_tiles, slots, false, st));
     return MOE_OK;
   }
-  MOE_HIP(launch_build_schedule(offsets, E, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags, (H + 255) / 256));
-  MOE_HIP(launch_gemm_fp8(up, true, p.max_tiles, st));
-  MOE_HIP(launch_gemm_fp8(down, false, p.max_tiles, st));
+  const bool halves = few_tiles_fp8(s, H);
+  MOE_HIP(launch_build_schedule(offsets, E, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags,
+                                halves ? 0 : (H + 255) / 256));
+  MOE_HIP(launch_gemm_fp8(up, true, false, p.max_tiles, st));
+  MOE_HIP(launch_gemm_fp8(down, false, halves, p.max_tiles, st));
   return MOE_OK;
 }
 
@@ -1747,12 +1755,13 @@ moe_status moe_grouped_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_
     MOE_HIP(launch_stream_fp8(g, false, false, num_experts, p.max_tiles, rows, y_dtype != MOE_F16, st));
     return MOE_OK;
   }
+  const bool halves = few_tiles_fp8(s, n);
   if (expert_offsets)
     MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags,
-                                  (n + 255) / 256));
+                                  halves ? 0 : (n + 255) / 256));
   else
     MOE_HIP(launch_clear_flags(flags, st));
-  MOE_HIP(launch_gemm_fp8(g, false, p.max_tiles, st));
+  MOE_HIP(launch_gemm_fp8(g, false, halves, p.max_tiles, st));
   return MOE_OK;
 }
 

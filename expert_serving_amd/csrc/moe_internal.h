@@ -332,8 +332,9 @@ struct Fp8Args {
   long long out_group;
   const int32_t* offsets; // streams: [E + 1]; null: rows [0, static_rows) of expert 0
 };
-// one matrix: y; dual (gate/up): h as codes and scales.  Row tiles of up to 256 rows.
-hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, int max_tiles, hipStream_t st);
+// one matrix: y; dual (gate/up): h as codes and scales.  Row tiles of up to 256 rows;
+// halves (one matrix): as two of up to 128, on 128 columns instead of 256.
+hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, bool halves, int max_tiles, hipStream_t st);
 // The products of few rows (stream_fp8.hip), 32-row tiles; max_tiles bounds them,
 // max_rows the rows of an expert.  dual: fp32 h.  quantise (one matrix, max_rows <= 16):
 // A holds fp32 h, quantised on the way (an h that is not finite sets MOE_FLAG_H_RANGE).
