@@ -67,16 +67,30 @@ __device__ __forceinline__ void wait_lds_and_loads() {
   __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));
 }
 
-// Logical index of this block among `real` tiles, XCD by XCD (block b runs on XCD
-// b % 8), so that every XCD gets a contiguous range; false behind the last.
-__device__ __forceinline__ bool xcd_index(int real, int& L) {
-  const int b = blockIdx.x;
-  const int per_xcd = (real + 7) >> 3;
-  const int slot = b >> 3;
-  if (slot >= per_xcd) return false;
-  L = (b & 7) * per_xcd + slot;
-  return L < real;
-}
+// The tiles of a launch, taken by blocks that stay: every XCD has an equal contiguous
+// share of them (blocks go to XCD blockIdx % 8 in turn, and neighbouring tiles share rows
+// and weights in its L2), a block whose XCD has none left helps the others, and the
+// quarter tiles of the last row tiles (see k_schedule_fp8) come behind all others.
+// Tiles differ in height, so equal counts alone leave XCDs idle: FFN of 8192 rows over 8
+// experts, 4096 x 14336, a third of the gate/up launch.
+struct Queue {
+  int32_t* next;    // [8] of the XCDs, [1] of the quarter tiles
+  int whole, all;   // tiles without quarters, and all
+  __device__ __forceinline__ int share(int x) const { return min(whole, (x + 1) * ((whole + 7) >> 3)); }
+  // tile of the own XCD's v-th turn, or one of another's; -1: none left
+  __device__ __forceinline__ int tile(int x, int v) const {
+    const int per = (whole + 7) >> 3;
+    if (x * per + v < share(x)) return x * per + v;
+    for (int i = 1; i < 8; ++i) {
+      const int y = (x + i) & 7, n = share(y) - y * per;
+      if (__hip_atomic_load(next + y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= n) continue;
+      const int u = atomicAdd(next + y, 1);
+      if (u < n) return y * per + u;
+    }
+    const int u = whole + atomicAdd(next + 8, 1);
+    return u < all ? u : -1;
+  }
+};
 
 __device__ __forceinline__ f32x16 mfma_scaled(i32x8 w, i32x8 x, f32x16 c, int ew, int ex) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 0, 0, 3, ew, 3, ex);
@@ -92,9 +106,10 @@ constexpr int tile_lds(int BM, int BN) {
 
 constexpr int max_of(int a, int b) { return a > b ? a : b; }
 
-// BM token rows x BN weight rows (DUAL: BN / 2 of each matrix).
+// BM token rows x BN weight rows (DUAL: BN / 2 of each matrix).  The first thread takes
+// its XCD's next turn (v) a few stages before the end.
 template <int BM, int BN, bool DUAL>
-__device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const MTile t, int ni) {
+__device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const MTile t, int ni, int32_t* turn, int& v) {
   constexpr int FM = BM / 64, FN = BN / 128;   // fragments of a wavefront: 2 x 4 wavefronts
   constexpr int WM = BM / 2, WN = DUAL ? BN / 8 : BN / 4;  // its rows and columns (of each matrix)
   constexpr int NI = FM + BN / 64;             // 8-row loads per wavefront and stage
@@ -226,6 +241,7 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
   int cur = 0;  // buffer of stage s
   for (int c = 0; c < S; c += kChunkStages) {
     load_scales(c / kChunkStages + 1);
+    if (BN == 256 && c + kChunkStages >= S && tid == 0) v = atomicAdd(turn, 1);
     for (int s = c; s < min(c + kChunkStages, S); ++s) {
       const int after = cur + 1 == NS ? 0 : cur + 1;
       // first step: the sums to this stage's units, the multiplications of one fragment
@@ -359,69 +375,164 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
   if (range && a.flags) atomicOr(a.flags, (uint32_t)(DUAL ? MOE_FLAG_H_RANGE : MOE_FLAG_Y_RANGE));
 }
 
-// Row tiles of up to 256 rows, each at the height its rows need; the blocks of an
-// expert's neighbouring row tiles come column by column (see the int8 form of the
-// same order).  BN 128: a row tile is taken as two of up to 128; such blocks fit a
-// compute unit twice.
-template <int BN, bool DUAL>
-__global__ __launch_bounds__(512, BN == 128 ? 4 : 2) void k_gemm_fp8(const Fp8Args a, int mslots, int ntiles) {
+// Tile L of the schedule's row tiles x cols columns: the tiles of an expert's
+// neighbouring row tiles come column by column, so that an XCD reads a weight column once
+// for all of them.
+__device__ __forceinline__ MTile tile_at(const MTile* __restrict__ sched, int L, int cols, int& col) {
+  const int at = L / cols, group = sched[at].group;
+  const int first = at - (group & 0xFF), size = group >> 8;
+  const int r = L - first * cols;
+  col = r / size;
+  MTile t = sched[first + (r - col * size)];
+  t.expert = __builtin_amdgcn_readfirstlane(t.expert);
+  t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+  t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+  col = __builtin_amdgcn_readfirstlane(col);
+  return t;
+}
+
+// Row tiles of up to 256 rows, each at the height its rows need, 256 weight rows.  One
+// block per compute unit; a block's first tile is its own, the others it draws.
+template <bool DUAL>
+__global__ __launch_bounds__(512) void k_gemm_fp8(const Fp8Args a, int cols) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  constexpr bool HALVES = BN == 128;
-  const int mtiles = a.sched ? min(*a.count, mslots) : mslots, cols = ntiles * (HALVES ? 2 : 1);
-  int L;
-  if (!xcd_index(mtiles * cols, L)) return;
-  const int at = L / cols;
-  int first, size;
-  if (a.sched) {
-    const int group = a.sched[at].group;
-    first = at - (group & 0xFF), size = group >> 8;
-  } else {
-    first = at / kTileGroup * kTileGroup, size = min(kTileGroup, mtiles - first);
-  }
-  const int r = L - first * cols, col = r / size, i = first + (r - col * size);
-  MTile t;
-  if (a.sched) t = a.sched[i];
-  else t = MTile{0, 256 * i, min(256, a.static_rows - 256 * i), 0};
-  int ni = col;
-  if constexpr (HALVES) {
-    ni = col >> 1;
-    t.row0 += 128 * (col & 1);
-    t.rows = min(t.rows - 128 * (col & 1), 128);
-  }
-  if (t.rows <= 0) return;
-  if (t.rows <= 64) {
-    tile_fp8<64, BN, DUAL>(smem, a, t, ni);
-  } else if (HALVES || t.rows <= 128) {
-    tile_fp8<128, BN, DUAL>(smem, a, t, ni);
-  } else if constexpr (!HALVES) {
-    if (t.rows <= 192) tile_fp8<192, BN, DUAL>(smem, a, t, ni);
-    else tile_fp8<256, BN, DUAL>(smem, a, t, ni);
+  constexpr int BN = 256;
+  const int x = blockIdx.x & 7;
+  int32_t* const next = a.count + (DUAL ? kFp8QueueUp : kFp8QueueDown);
+  const Queue queue{next, a.count[1] * cols, a.count[0] * cols};
+  int32_t* const s_tile = reinterpret_cast<int32_t*>(smem);
+  int v = blockIdx.x >> 3;  // (the queues begin behind the blocks' own turns)
+  for (;;) {
+    if (threadIdx.x == 0) *s_tile = queue.tile(x, v);
+    __syncthreads();
+    const int L = __builtin_amdgcn_readfirstlane(*s_tile);
+    __syncthreads();  // (the tile's loads overwrite it)
+    if (L < 0) return;
+    int ni;
+    const MTile t = tile_at(a.sched, L, cols, ni);
+    if (t.rows <= 0) {  // (a quarter behind a short tile)
+      if (threadIdx.x == 0) v = atomicAdd(next + x, 1);
+    } else if (t.rows <= 64) {
+      tile_fp8<64, BN, DUAL>(smem, a, t, ni, next + x, v);
+    } else if (t.rows <= 128) {
+      tile_fp8<128, BN, DUAL>(smem, a, t, ni, next + x, v);
+    } else if (t.rows <= 192) {
+      tile_fp8<192, BN, DUAL>(smem, a, t, ni, next + x, v);
+    } else {
+      tile_fp8<256, BN, DUAL>(smem, a, t, ni, next + x, v);
+    }
+    __syncthreads();
   }
 }
 
-template <int BN, bool DUAL>
-hipError_t launch_tiles(const Fp8Args& a, int max_tiles, hipStream_t st) {
-  const int mslots = a.sched ? max_tiles : (a.static_rows + 255) / 256;
-  if (mslots <= 0) return hipSuccess;
-  constexpr int lds = BN == 128 ? max_of(tile_lds(64, BN), tile_lds(128, BN))
-                                : max_of(tile_lds(128, BN), tile_lds(256, BN));  // (64 and 192 rows take less)
-  static_assert(lds <= 160 * 1024 / (BN == 128 ? 2 : 1), "LDS");
-  static std::atomic<uint64_t> set_on{0};
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(&k_gemm_fp8<BN, DUAL>), lds, set_on);
+// The same on 128 weight rows, a row tile taken as two of up to 128: for launches of few
+// tiles, one each of blocks that fit a compute unit twice.
+__global__ __launch_bounds__(512, 4) void k_gemm_fp8_halves(const Fp8Args a, int cols) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int real = a.count[0] * 2 * cols, per = (real + 7) >> 3, slot = blockIdx.x >> 3;
+  const int L = (blockIdx.x & 7) * per + slot;  // (an XCD's share, as in a queue)
+  if (slot >= per || L >= real) return;
+  int col, none = 0;
+  MTile t = tile_at(a.sched, L, 2 * cols, col);
+  t.row0 += 128 * (col & 1);
+  t.rows = min(t.rows - 128 * (col & 1), 128);
+  if (t.rows <= 0) return;
+  if (t.rows <= 64) tile_fp8<64, 128, false>(smem, a, t, col >> 1, nullptr, none);
+  else tile_fp8<128, 128, false>(smem, a, t, col >> 1, nullptr, none);
+}
+
+template <typename F>
+hipError_t launch_tiles(F* kernel, int lds, std::atomic<uint64_t>& set_on, long long grid, const Fp8Args& a, int cols,
+                        hipStream_t st) {
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), lds, set_on);
   if (e != hipSuccess) return e;
-  constexpr int cols = DUAL ? BN / 2 : BN;
-  const int ntiles = (a.N + cols - 1) / cols;
-  const long long grid = ((long long)mslots * ntiles * (BN == 128 ? 2 : 1) + 7) / 8 * 8;
   if (grid > 0x7fffff) return hipErrorInvalidValue;  // (2^32 threads of one axis)
-  hipLaunchKernelGGL((k_gemm_fp8<BN, DUAL>), dim3((unsigned)grid), dim3(512), lds, st, a, mslots, ntiles);
+  hipLaunchKernelGGL(*kernel, dim3((unsigned)grid), dim3(512), lds, st, a, cols);
   return hipGetLastError();
+}
+
+// Row tiles of up to 256 rows in expert order, the queues at their beginning and the flag
+// word cleared.  fill_cols > 0: the column tiles of a launch; when a few rounds of its tiles on
+// all compute units would end with one that keeps at most a quarter of them busy, that
+// round's row tiles are cut into kFillSplit (some parts without rows).
+// offsets null: rows [0, static_rows) of one expert.
+__global__ __launch_bounds__(512) void k_schedule_fp8(const int32_t* __restrict__ offsets, int E, int static_rows,
+                                                      MTile* __restrict__ sched, int max_tiles,
+                                                      int32_t* __restrict__ count, uint32_t* __restrict__ flags,
+                                                      int fill_cols) {
+  __shared__ int s_wave[8];
+  const int tid = threadIdx.x, lane = tid & 63;
+  if (tid == 0) *flags = 0u;
+  if (tid >= 2 && tid < kFp8CountWords)
+    count[tid] = (tid - kFp8QueueUp) < 8u || (tid - kFp8QueueDown) < 8u ? kUnits / 8 : 0;
+  int r0 = 0, kept = 0;
+  if (tid < E) {
+    r0 = offsets ? offsets[tid] : 0;
+    kept = (offsets ? offsets[tid + 1] : static_rows) - r0;
+  }
+  const int nb = (kept + 255) / 256;
+  int upto = nb;  // tiles of the experts up to this one
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int o = __shfl_up(upto, off, 64);
+    if (lane >= off) upto += o;
+  }
+  if (lane == 63) s_wave[tid >> 6] = upto;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < (tid >> 6)) upto += s_wave[w];
+    total += s_wave[w];
+  }
+  int whole = total;
+  if (fill_cols > 0) {
+    const long long blocks = (long long)total * fill_cols;
+    const int rest = (int)(blocks % kUnits), turn = (rest + fill_cols - 1) / fill_cols;
+    if (rest > 0 && blocks > kUnits && blocks < 5 * kUnits && turn * fill_cols * kFillSplit <= kUnits)
+      whole = total - turn;
+  }
+  const int begin = upto - nb, uncut = min(max(whole - begin, 0), nb);
+  for (int i = 0; i < nb; ++i) {
+    const int slot = begin + i;
+    if (i < uncut) {
+      const int g = i / kTileGroup * kTileGroup;
+      if (slot < max_tiles)
+        sched[slot] = MTile{tid, r0 + 256 * i, min(256, kept - 256 * i), tile_group(i - g, min(kTileGroup, uncut - g))};
+    } else {
+      constexpr int part = 256 / kFillSplit;
+      for (int q = 0; q < kFillSplit; ++q) {
+        const int at = whole + (slot - whole) * kFillSplit + q;
+        if (at < max_tiles)
+          sched[at] = MTile{tid, r0 + 256 * i + q * part, max(0, min(part, kept - 256 * i - q * part)),
+                            tile_group(q, kFillSplit)};
+      }
+    }
+  }
+  if (tid == 0) {
+    count[0] = min(whole + (total - whole) * kFillSplit, max_tiles);
+    count[1] = min(whole, max_tiles);
+  }
 }
 
 }  // namespace
 
+hipError_t launch_schedule_fp8(const int32_t* offsets, int E, int static_rows, MTile* sched, int max_tiles,
+                               int32_t* count, uint32_t* flags, int fill_cols, hipStream_t st) {
+  hipLaunchKernelGGL(k_schedule_fp8, dim3(1), dim3(512), 0, st, offsets, E, static_rows, sched, max_tiles, count,
+                     flags, fill_cols);
+  return hipGetLastError();
+}
+
 hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, bool halves, int max_tiles, hipStream_t st) {
-  if (dual) return launch_tiles<256, true>(a, max_tiles, st);
-  return halves ? launch_tiles<128, false>(a, max_tiles, st) : launch_tiles<256, false>(a, max_tiles, st);
+  static std::atomic<uint64_t> set_up{0}, set_down{0}, set_halves{0};
+  constexpr int lds = max_of(tile_lds(128, 256), tile_lds(256, 256));  // (64 and 192 rows take less)
+  constexpr int lds_halves = max_of(tile_lds(64, 128), tile_lds(128, 128));
+  static_assert(lds <= 160 * 1024 && lds_halves <= 80 * 1024, "LDS");
+  if (dual) return launch_tiles(k_gemm_fp8<true>, lds, set_up, kUnits, a, (a.N + 127) / 128, st);
+  if (!halves) return launch_tiles(k_gemm_fp8<false>, lds, set_down, kUnits, a, (a.N + 255) / 256, st);
+  const int cols = (a.N + 127) / 128;
+  return launch_tiles(k_gemm_fp8_halves, lds_halves, set_halves, ((long long)max_tiles * 2 * cols + 7) / 8 * 8, a, cols, st);
 }
 
 }  // namespace moe

@@ -854,7 +854,6 @@ moe_status check_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t E) {
 }
 
 struct Fp8Plan {
-  GemmPlan gp;
   bool stream;
   int max_tiles;  // row tiles, of the stream's height where it is one
   size_t flags, sched, sched_count, h, hq, hsc, total;
@@ -876,9 +875,6 @@ Fp8Plan plan_fp8(const moe_shape& s, bool ffn) {
   const long long rows = (long long)s.num_tokens * s.top_k, H = s.hidden, I = s.intermediate;
   const int E = s.num_experts;
   p.stream = rows > 0 && (ffn ? stream_fp8(s, 3 * H * I, (2 * H + I) / 3) : stream_fp8(s, H * I, I));
-  p.gp.bm_big = 256;
-  p.gp.bm_small = 32;
-  p.gp.split_rows = 0;
   p.max_tiles = p.stream ? (int)stream_tiles(s) : (int)(rows / 256 + E + 1) + kUnits;  // (cut tiles)
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -888,7 +884,7 @@ Fp8Plan plan_fp8(const moe_shape& s, bool ffn) {
   };
   p.flags = take(256);
   p.sched = take(p.stream ? 0 : (size_t)p.max_tiles * sizeof(MTile));
-  p.sched_count = take(16);
+  p.sched_count = take(kFp8CountWords * 4);
   if (ffn) {
     p.h = take(p.stream ? (size_t)rows * I * 4 : 0);
     p.hq = take((size_t)rows * I);
@@ -937,8 +933,7 @@ moe_status run_ffn_fp8(const moe_shape& s, const void* x, const float* xsc, cons
     return MOE_OK;
   }
   const bool halves = few_tiles_fp8(s, H);
-  MOE_HIP(launch_build_schedule(offsets, E, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags,
-                                halves ? 0 : (H + 255) / 256));
+  MOE_HIP(launch_schedule_fp8(offsets, E, 0, sched, p.max_tiles, count, flags, halves ? 0 : (H + 255) / 256, st));
   MOE_HIP(launch_gemm_fp8(up, true, false, p.max_tiles, st));
   MOE_HIP(launch_gemm_fp8(down, false, halves, p.max_tiles, st));
   return MOE_OK;
@@ -1745,7 +1740,7 @@ moe_status moe_grouped_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_
   if (rows == 0) return MOE_OK;
   hipStream_t st = static_cast<hipStream_t>(stream);
   uint32_t* flags = at<uint32_t>(ws, p.flags);
-  MTile* sched = expert_offsets ? at<MTile>(ws, p.sched) : nullptr;
+  MTile* sched = at<MTile>(ws, p.sched);
   int32_t* count = at<int32_t>(ws, p.sched_count);
   const Fp8Args g{static_cast<const uint8_t*>(a), a_scales, k / 128, 1, static_cast<const uint8_t*>(b), nullptr,
                   b_scales, nullptr, n, k, y, y_dtype, sched, count, rows, flags, nullptr, 0, expert_offsets};
@@ -1756,11 +1751,8 @@ moe_status moe_grouped_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_
     return MOE_OK;
   }
   const bool halves = few_tiles_fp8(s, n);
-  if (expert_offsets)
-    MOE_HIP(launch_build_schedule(expert_offsets, num_experts, p.gp, sched, p.max_tiles, nullptr, 0, count, st, flags,
-                                  halves ? 0 : (n + 255) / 256));
-  else
-    MOE_HIP(launch_clear_flags(flags, st));
+  MOE_HIP(launch_schedule_fp8(expert_offsets, num_experts, rows, sched, p.max_tiles, count, flags,
+                              halves ? 0 : (n + 255) / 256, st));
   MOE_HIP(launch_gemm_fp8(g, false, halves, p.max_tiles, st));
   return MOE_OK;
 }

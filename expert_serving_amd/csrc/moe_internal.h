@@ -324,17 +324,22 @@ struct Fp8Args {
   int N, K;
   void* out;
   int y_dtype;            // MOE_F16 or MOE_BF16 (one matrix)
-  const MTile* sched;     // row tiles; null: rows [0, static_rows) of expert 0
-  const int32_t* count;
-  int static_rows;
+  const MTile* sched;     // row tiles, their number and the queues (launch_schedule_fp8)
+  int32_t* count;
+  int static_rows;        // streams without offsets
   uint32_t* flags;
   float* out_scales;      // gate/up: scale of h row r, group g at g * out_group + r
   long long out_group;
   const int32_t* offsets; // streams: [E + 1]; null: rows [0, static_rows) of expert 0
 };
 // one matrix: y; dual (gate/up): h as codes and scales.  Row tiles of up to 256 rows;
-// halves (one matrix): as two of up to 128, on 128 columns instead of 256.
+// halves (one matrix): as two of up to 128, on 128 columns instead of 256.  A schedule
+// serves one launch of either kind.
 hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, bool halves, int max_tiles, hipStream_t st);
+// count: all tiles, those before the quarter tiles, and a queue for each kind of launch
+constexpr int kFp8QueueUp = 4, kFp8QueueDown = 16, kFp8CountWords = 32;
+hipError_t launch_schedule_fp8(const int32_t* offsets, int E, int static_rows, MTile* sched, int max_tiles,
+                               int32_t* count, uint32_t* flags, int fill_cols, hipStream_t st);
 // The products of few rows (stream_fp8.hip), 32-row tiles; max_tiles bounds them,
 // max_rows the rows of an expert.  dual: fp32 h.  quantise (one matrix, max_rows <= 16):
 // A holds fp32 h, quantised on the way (an h that is not finite sets MOE_FLAG_H_RANGE).
