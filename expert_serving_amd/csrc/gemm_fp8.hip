@@ -35,19 +35,14 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 typedef const __attribute__((address_space(1))) void* gbl_ptr_t;
 
 constexpr int kBufferRsrcWord3 = 0x00020000;  // raw buffer of gfx9-family GPUs, 32-bit data format
 constexpr int kStage = 128;                   // codes (bytes) of K per stage
 constexpr int kChunkStages = 8;               // stages whose scales lie in LDS together
-
-__device__ __forceinline__ uint32_t f16_bits(float f) { return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f); }
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-  const uint32_t b = __float_as_uint(f);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return (b >> 16) | 0x40u;  // NaN stays NaN
-  return (b + (((b >> 16) & 1u) + 0x7FFFu)) >> 16;
-}
 
 // the 32 codes of a lane for v_mfma_scale_f32_32x32x64_f8f6f4, from two 16-byte parts
 __device__ __forceinline__ i32x8 cat8(u32x4 lo, u32x4 hi) {
@@ -335,31 +330,34 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
     constexpr int WC = FN * 32, CH = WC / 8;
     uint16_t* const part = reinterpret_cast<uint16_t*>(smem) + wave * (WM * WC);
     auto place = [&](int row, int ch) { return row * WC + ((ch ^ (CH == 8 ? row & 7 : (row >> 1) & 3)) << 3); };
+    auto lay = [&](auto f16) {
 #pragma unroll
-    for (int b = 0; b < FM; ++b) {
-      const bool real = wm * WM + b * 32 + fr < rows;
+      for (int b = 0; b < FM; ++b) {
+        const bool real = wm * WM + b * 32 + fr < rows;
 #pragma unroll
-      for (int f = 0; f < FN; ++f) {
-        const float u = f8_unit_of(et[b]) * f8_unit_of(ew[f]);
+        for (int f = 0; f < FN; ++f) {
+          const float u = f8_unit_of(et[b]) * f8_unit_of(ew[f]);
 #pragma unroll
-        for (int qi = 0; qi < 4; ++qi) {
-          const bool in = n0 + wn * WC + f * 32 + 8 * qi < N;
-          uint32_t w[4];
+          for (int qi = 0; qi < 4; ++qi) {
+            f32x4 v;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float v = acc[f][b][4 * qi + q] * u;
-            if (a.y_dtype == MOE_F16) {
-              range |= real && in && !(fabsf(v) <= 65504.f);
-              w[q] = f16_bits(v);
+            for (int q = 0; q < 4; ++q) v[q] = acc[f][b][4 * qi + q] * u;
+            u32x2 w;
+            if constexpr (f16.value) {
+              const bool in = n0 + wn * WC + f * 32 + 8 * qi < N;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) range |= real && in && !(fabsf(v[q]) <= 65504.f);
+              w = __builtin_bit_cast(u32x2, __builtin_convertvector(v, f16x4));
             } else {
-              w[q] = bf16_bits(v);
+              w = __builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4));
             }
+            *reinterpret_cast<u32x2*>(part + place(b * 32 + fr, f * 4 + qi) + 4 * fk) = w;
           }
-          *reinterpret_cast<u32x2*>(part + place(b * 32 + fr, f * 4 + qi) + 4 * fk) =
-              u32x2{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
         }
       }
-    }
+    };
+    if (a.y_dtype == MOE_F16) lay(std::true_type{});
+    else lay(std::false_type{});
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     constexpr int RPL = 64 / CH;
