@@ -38,6 +38,10 @@ __device__ __forceinline__ uint32_t bf16_bits(float f) {
   return (b + (((b >> 16) & 1u) + 0x7FFFu)) >> 16;
 }
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
+}
+
 struct Tile {
   int expert, row0, rows;
 };
@@ -101,20 +105,23 @@ __device__ __forceinline__ void stream_tile(float* __restrict__ smem, const Fp8A
   const int steps = K / kStep;
   const int mine = wave < steps ? (steps - wave + kWaves - 1) / kWaves : 0;
 
-  const uint8_t* wp[NB][F];
-  const uint8_t* ap[MH];
+  // Buffer loads: a resource for each expert's matrix, the tile's rows and their scales,
+  // a 32-bit offset per fragment (an expert's matrix and 32 rows of at most 2^20 values
+  // are below 2^31 bytes) and the step's in a scalar register.
+  const size_t eb = (size_t)t.expert * N * K;
+  const __amdgpu_buffer_rsrc_t rw[2] = {resource(a.B0 + eb, (uint32_t)N * (uint32_t)K),
+                                        resource((DUAL ? a.B1 : a.B0) + eb, (uint32_t)N * (uint32_t)K)};
+  constexpr int kBytes = QUANT ? 4 : 1;
+  const __amdgpu_buffer_rsrc_t ra = resource(a.A + (size_t)t.row0 * K * kBytes, (uint32_t)t.rows * (uint32_t)K * kBytes);
+  int wo[F], ao[MH];
+#pragma unroll
+  for (int f = 0; f < F; ++f) wo[f] = min(n0 + 16 * f + lr, N - 1) * K + wave * kStep + lk;
   const float* sp[MH];
 #pragma unroll
-  for (int f = 0; f < F; ++f) {
-    const size_t o = ((size_t)t.expert * N + min(n0 + 16 * f + lr, N - 1)) * K + (size_t)wave * kStep + lk;
-    wp[0][f] = a.B0 + o;
-    if constexpr (DUAL) wp[NB - 1][f] = a.B1 + o;
-  }
-#pragma unroll
   for (int h = 0; h < MH; ++h) {
-    const int r = t.row0 + min(16 * h + lr, t.rows - 1);
-    ap[h] = a.A + ((size_t)r * K + (size_t)wave * kStep + lk) * (QUANT ? 4 : 1);
-    sp[h] = QUANT ? nullptr : a.sa + (size_t)r * a.sa_row + (size_t)wave * a.sa_group;
+    const int r = min(16 * h + lr, t.rows - 1);
+    ao[h] = (r * K + wave * kStep + lk) * kBytes;
+    sp[h] = QUANT ? nullptr : a.sa + (size_t)(t.row0 + r) * a.sa_row + (size_t)wave * a.sa_group;
   }
   // (a block's columns lie in one block of 128 weight rows: 16 F divides 128)
   const size_t so = ((size_t)t.expert * ((N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block) * steps + wave;
@@ -133,7 +140,7 @@ __device__ __forceinline__ void stream_tile(float* __restrict__ smem, const Fp8A
   bool range = false;
   auto issue = [&](int d, int s) {  // step s of this wavefront (past the last: re-read, not used)
     const int at = min(s, mine - 1) * kWaves;
-    const size_t o = (size_t)at * kStep;
+    const int o = at * kStep;
 #pragma unroll
     for (int m = 0; m < NB; ++m) sb[d][m] = __float_as_uint(sw[m][at]);
 #pragma unroll
@@ -141,7 +148,7 @@ __device__ __forceinline__ void stream_tile(float* __restrict__ smem, const Fp8A
 #pragma unroll
       for (int m = 0; m < NB; ++m)
 #pragma unroll
-        for (int f = 0; f < F; ++f) wv[d][m][f][q] = *reinterpret_cast<const u32x4*>(wp[m][f] + o + 64 * q);
+        for (int f = 0; f < F; ++f) wv[d][m][f][q] = __builtin_amdgcn_raw_buffer_load_b128(rw[m], wo[f], o + 64 * q, 0);
 #pragma unroll
     for (int h = 0; h < MH; ++h) {
       if constexpr (QUANT) {
@@ -149,7 +156,8 @@ __device__ __forceinline__ void stream_tile(float* __restrict__ smem, const Fp8A
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[q][i] = *reinterpret_cast<const f32x4*>(ap[h] + (o + 64 * q) * 4 + 16 * i);
+          for (int i = 0; i < 4; ++i)
+            v[q][i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, ao[h] + 16 * i, (o + 64 * q) * 4, 0));
         uint32_t top = 0u;
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -171,7 +179,7 @@ __device__ __forceinline__ void stream_tile(float* __restrict__ smem, const Fp8A
         sr[d][h] = __float_as_uint(f8_scale(amax));
       } else {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) av[d][h][q] = *reinterpret_cast<const u32x4*>(ap[h] + o + 64 * q);
+        for (int q = 0; q < 2; ++q) av[d][h][q] = __builtin_amdgcn_raw_buffer_load_b128(ra, ao[h], o + 64 * q, 0);
         sr[d][h] = __float_as_uint(sp[h][(size_t)at * a.sa_group]);
       }
     }
@@ -196,26 +204,34 @@ __device__ __forceinline__ void stream_tile(float* __restrict__ smem, const Fp8A
 #pragma unroll
           for (int q = 0; q < 4; ++q) acc[m][f][h][q] = fmaf(p[q], u, acc[m][f][h][q]);
         }
+        __builtin_amdgcn_sched_barrier(0);  // (few block sums at a time: registers)
       }
     }
   };
   if (mine > 0) {
 #pragma unroll
     for (int d = 0; d < D; ++d) issue(d, d);
-    const int full = mine - mine % D;
-    for (int s = 0; s < full; s += D) {
+    // no branch around a load inside the loop: its result would be copied at the join,
+    // and the copy waits for it
+    int s = 0;
+    for (; s + 2 * D <= mine; s += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         // the fences keep the next loads below the products that free their registers
         multiply(d);
         __builtin_amdgcn_sched_barrier(0);
-        if (s + d + D < mine) issue(d, s + d + D);
+        issue(d, s + d + D);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
 #pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (s + d < mine) multiply(d);
+      if (s + d + D < mine) issue(d, s + d + D);
+    }
+#pragma unroll
     for (int d = 0; d < D; ++d)
-      if (d < mine - full) multiply(d);
+      if (s + d + D < mine) multiply(d);
   }
   if (QUANT && range && n0 == 0 && a.flags) atomicOr(a.flags, (uint32_t)MOE_FLAG_H_RANGE);
 
