@@ -859,14 +859,44 @@ struct Fp8Plan {
   size_t flags, sched, sched_count, h, hq, hsc, total;
 };
 
-// Products of fewer than 64 rows per expert stream their weights while the 32-row tiles
-// together read at most 240 MB, and at most 120 KB per k of their (mean) K.
-bool stream_fp8(const moe_shape& s, long long matrix_bytes, long long mean_k) { return stream_i8(s, matrix_bytes, mean_k); }
+// 8-bit floating-point products of fewer than 64 rows per expert stream their weights
+// (launch_stream_fp8) while the 32-row tiles together read at most 200 KB per k of their
+// (mean) K, or 40 KB where an expert has more than 16 rows and a step multiplies two
+// halves: the wavefronts of a stream share K and have too little of a short one, and a
+// second half costs a stream more than the LDS tiles.  Measured, streams against LDS
+// tiles: FFN of 1 token over 128 experts of 2048 x 768 (36 MB) 16 against 36 us, of 8
+// tokens (297 MB) 79 against 82, of 16 (594 MB) 120 against 107; of 2 tokens over 256
+// experts of 7168 x 2048 (672 MB) 137 against 144, of 4 (1386 MB) 268 against 255; of 8
+// tokens over 8 experts of 4096 x 14336 (1344 MB) 238 against 269, of 64 (2016 MB) 312
+// against 298; product of 128 rows, 8 experts, 4096 x 14336 (672 MB) 88 against 115; of
+// 300 rows, 64 experts, 1024 x 1024 (73 MB) 26 against 27, 128 experts (137 MB) 48
+// against 42.  More than 16 rows: of 300, 16 experts, 1024 x 1024 (25 MB) 9.1 against
+// 10.9, of 600, 32 experts (50 MB) 16.4 against 12.8; of 400, 16 experts, 2048 x 2048
+// (112 MB) 24 against 20; of 60, 1 expert, 14336 x 4096 (112 MB) 31 against 33; of 700,
+// 32 experts, 1024 x 4096 (212 MB) 31 against 29; of 60, 1 expert, 28672 x 8192 (448 MB)
+// 109 against 85.
+bool stream_fp8(const moe_shape& s, long long matrix_bytes, long long mean_k) {
+  const long long slots = (long long)s.num_tokens * s.top_k, E = s.num_experts;
+  if (slots / E >= 64) return false;
+  return stream_tiles(s) * matrix_bytes <= mean_k * ((slots > 16 * E ? 40LL : 200LL) << 10);
+}
 
+// A launch of single products on 128 x 128 tiles, two of a compute unit, instead of up to
+// 256 x 256 ones: where the estimated larger tiles (experts' last ones are short) would
+// take less than half the compute units, or five eighths where experts have more than 128
+// rows, so that the larger tile is a tall one and a smaller tile halves its time.
+// Measured, 128 x 128 against 256 x 256: products of 1024 rows x 4096 x 4096 (64 tiles) 34
+// against 59 us, 2000 rows (128) 51 against 64, 2600 (160) 71 against 67; of 3000 rows, 16
+// experts, 2048 x 2048 (152) 28 against 39; of 1500 rows, 8 experts, 4096 x 14336 (144) 171
+// against 214; 1280 rows x 8192 x 8192 (160) 122 against 108.  Experts of at most 128 rows:
+// 700 rows, 4 experts, 4096 x 4096 (64) 32 against 48; 800, 8 experts, 3584 x 2048 (112) 24
+// against 27; 600, 8 experts, 4096 x 4096 (128) 43 against 40, x 14336 164 against 133;
+// 400, 4 experts, 8192 x 8192 (128) 92 against 74.  The rule costs 256 rows x 28672 x 4096
+// (112), where a tile's weights serve twice the rows: 82 against 59.
 bool few_tiles_fp8(const moe_shape& s, int n) {
   const long long slots = (long long)s.num_tokens * s.top_k, E = s.num_experts;
   const long long tiles = std::max(slots / 256 + (E + 1) / 2, std::min(slots, E));
-  return tiles * ((n + 255) / 256) < kComputeUnits * 2 / 3;
+  return tiles * ((n + 255) / 256) < (slots <= 128 * E ? kComputeUnits / 2 : kComputeUnits * 5 / 8);
 }
 
 // a batch of one slot per row of n columns and K = k, or (inter > 0) the FFN of a shape
@@ -922,6 +952,11 @@ moe_status run_ffn_fp8(const moe_shape& s, const void* x, const float* xsc, cons
     float* h = at<float>(ws, p.h);
     up.out = h;
     MOE_HIP(launch_stream_fp8(up, true, false, E, p.max_tiles, slots, true, st));
+    // Quantised by the second product or by a launch, measured: FFN of 1 token over 128
+    // experts of 2048 x 768 16.0 against 17.6 us, of 2 tokens 27.2 against 25.7; of 16 rows
+    // over 8 experts of 1024 x 1024 14.6 against 16.1, of 8 of 2048 x 2048 17.7 against 19.5;
+    // of 1 token over 256 experts of 7168 x 2048 75.7 against 72.6, over 8 of 4096 x 14336
+    // (not fused) 74.3 against 72.9.
     const bool fused = stream_quantises(slots, I);
     if (fused) {
       down.A = reinterpret_cast<const uint8_t*>(h);
