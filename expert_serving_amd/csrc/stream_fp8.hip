@@ -16,6 +16,20 @@
 //     touches every 64-byte sector once.  Rows and weights use the same split of K over
 //     lanes and bytes, so each product pairs equal k;
 //   * the eight partial sums meet in LDS and are added in order.
+// Gate and up of few rows multiply the codes as fp16, which holds each, on
+// v_mfma_f32_16x16x32_f16 instead: the 8-bit units drop what lies 2^-13 below a group's
+// largest product, and an h off by 1.4e-5 for that now and then rounds to the next of its 8-bit
+// codes, half a step from where it was.  Large batches average over such codes, in the
+// row of one token a single one showed (2-norm error of y 4.3e-3 instead of the 1.6e-3 that
+// bf16 leaves).  16 conversions and four multiplications for one: 0 to 8 % of the FFN, for which
+// the memory sets the time.
+// D = 2 steps are under way per wavefront (a third adds 12 % to the product of 17 rows below,
+// a fourth 3 %: fewer blocks per compute unit).
+//
+// Measured (device time of calls in a row): product of 17 rows x 14336 x 4096 15 us, weights
+// at 3.9 TB/s; of 128 rows, 8 experts, 4096 x 14336 88 us, 5.3 TB/s; of 1 row x 4096 x 4096
+// 8 us; FFN of 1 token over 128 experts of 2048 x 768 16 us for 38 MB, which is the
+// latency of two launches, a tile search, a chain of loads and a join each.
 #include "moe_internal.h"
 #include "quant_fp8.h"
 #include "swiglu.h"
@@ -26,6 +40,8 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kWaves = 8;
 constexpr int kStep = 128;  // codes of a step
@@ -116,12 +132,14 @@ __device__ __forceinline__ void stream_tile(float* __restrict__ smem, const Fp8A
   int wo[F], ao[MH];
 #pragma unroll
   for (int f = 0; f < F; ++f) wo[f] = min(n0 + 16 * f + lr, N - 1) * K + wave * kStep + lk;
-  const float* sp[MH];
+  // (their scales row-major, as every caller of a stream has them)
+  const __amdgpu_buffer_rsrc_t rs = resource(a.sa + (size_t)t.row0 * steps, (uint32_t)t.rows * (uint32_t)steps * 4);
+  int so_row[MH];
 #pragma unroll
   for (int h = 0; h < MH; ++h) {
     const int r = min(16 * h + lr, t.rows - 1);
     ao[h] = (r * K + wave * kStep + lk) * kBytes;
-    sp[h] = QUANT ? nullptr : a.sa + (size_t)(t.row0 + r) * a.sa_row + (size_t)wave * a.sa_group;
+    so_row[h] = (r * steps + wave) * 4;
   }
   // (a block's columns lie in one block of 128 weight rows: 16 F divides 128)
   const size_t so = ((size_t)t.expert * ((N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block) * steps + wave;
@@ -180,7 +198,7 @@ __device__ __forceinline__ void stream_tile(float* __restrict__ smem, const Fp8A
       } else {
 #pragma unroll
         for (int q = 0; q < 2; ++q) av[d][h][q] = __builtin_amdgcn_raw_buffer_load_b128(ra, ao[h], o + 64 * q, 0);
-        sr[d][h] = __float_as_uint(sp[h][(size_t)at * a.sa_group]);
+        sr[d][h] = __builtin_amdgcn_raw_buffer_load_b32(rs, so_row[h], at * 4, 0);
       }
     }
   };
@@ -188,7 +206,48 @@ __device__ __forceinline__ void stream_tile(float* __restrict__ smem, const Fp8A
     return i32x8{(int)p[0][0], (int)p[0][1], (int)p[0][2], (int)p[0][3],
                  (int)p[1][0], (int)p[1][1], (int)p[1][2], (int)p[1][3]};
   };
+  auto halves = [](uint32_t a, uint32_t b) {
+    f16x8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = i < 2 ? a : b;
+      const f16x2 p = i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, true)
+                            : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, false);
+      r[2 * i] = p[0], r[2 * i + 1] = p[1];
+    }
+    return r;
+  };
+  // not finite counts as NaN
+  auto finite = [](uint32_t scale) {
+    return __uint_as_float((scale & 0x7F800000u) == 0x7F800000u ? 0x7FC00000u : scale);
+  };
+  auto multiply_wide = [&](int d) {
+#pragma unroll
+    for (int h = 0; h < MH; ++h) {
+      f16x8 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = halves(av[d][h][i >> 1][2 * (i & 1)], av[d][h][i >> 1][2 * (i & 1) + 1]);
+      const float scale = finite(sr[d][h]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < NB; ++m) {
+        const float sm = finite(sb[d][m]);
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          f32x4 p{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            p = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                halves(wv[d][m][f][i >> 1][2 * (i & 1)], wv[d][m][f][i >> 1][2 * (i & 1) + 1]), x[i], p, 0, 0, 0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[m][f][h][q] = fmaf(p[q] * scale, sm, acc[m][f][h][q]);
+          __builtin_amdgcn_sched_barrier(0);  // (few block sums at a time: registers)
+        }
+      }
+    }
+  };
   auto multiply = [&](int d) {
+    if constexpr (DUAL) return multiply_wide(d);
 #pragma unroll
     for (int m = 0; m < NB; ++m) {
       const float um = f8_unit(sb[d][m]);
@@ -304,8 +363,11 @@ hipError_t launch(const Fp8Args& a, int E, bool clear_flags, int tiles, hipStrea
   return hipGetLastError();
 }
 
-// blocks below which 32 columns per block are better than 64: they leave compute units
-// idle
+// Blocks below which 32 columns per block are better than 64, which leave compute units
+// idle.  Measured, 64 against 32 columns: product of 1 row x 4096 x 4096 (64 wide blocks)
+// 11.6 against 8.0 us, x 8192 (128) 11.8 against 7.8, x 12288 (192) 12.2 against 11.9, of 28672 x 8192
+// (448) 42 against 56; of 17 rows x 8192 x 4096 (128) 14.3 against 11.0, x 14336 (224) 14.7
+// against 17.7; of 64 rows, 16 experts, 4096 x 1024 25 against 28.
 constexpr int kWideBlocks = 192;
 
 }  // namespace

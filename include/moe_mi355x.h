@@ -514,6 +514,7 @@ moe_status moe_grouped_ffn_int8(const moe_shape* shape, const int8_t* x_codes, c
  * their norm for that (measured), far below half a step of the 16-bit types
  * (fp16 2^-11, bf16 2^-8), so the products are written in those: y_dtype is
  * MOE_F16 or MOE_BF16, MOE_F32 is MOE_ERR_UNSUPPORTED.
+ * Scales are not negative (the sign of one is unspecified in a product).
  * A block with an infinity or NaN gets unspecified codes and a scale that is not
  * finite (NaN for a NaN); a row of a product with such a scale, or with a NaN
  * code, is NaN, as is a column of such a weight block.  A scale
