@@ -217,21 +217,23 @@ __device__ __forceinline__ void stream_tile(float* __restrict__ smem, const Fp8A
     }
     return r;
   };
-  // not finite counts as NaN
-  auto finite = [](uint32_t scale) {
-    return __uint_as_float((scale & 0x7F800000u) == 0x7F800000u ? 0x7FC00000u : scale);
-  };
+  // significand of a scale, NaN for one that is not finite, and its exponent + 127; the exponents
+  // of the two scales meet before they are applied, as they do in the 8-bit units: neither alone
+  // leaves the range
+  auto unit = [](uint32_t scale) { return (scale & 0x7F800000u) == 0x7F800000u ? __uint_as_float(0x7FC00000u) : f8_unit(scale); };
+  auto power = [](uint32_t scale) { return (int)((scale >> 23) & 0xFFu); };
   auto multiply_wide = [&](int d) {
 #pragma unroll
     for (int h = 0; h < MH; ++h) {
       f16x8 x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = halves(av[d][h][i >> 1][2 * (i & 1)], av[d][h][i >> 1][2 * (i & 1) + 1]);
-      const float scale = finite(sr[d][h]);
+      const float ux = unit(sr[d][h]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int m = 0; m < NB; ++m) {
-        const float sm = finite(sb[d][m]);
+        const float u = ux * unit(sb[d][m]);
+        const int e = power(sr[d][h]) + power(sb[d][m]) - 254;
 #pragma unroll
         for (int f = 0; f < F; ++f) {
           f32x4 p{0.f, 0.f, 0.f, 0.f};
@@ -240,7 +242,7 @@ __device__ __forceinline__ void stream_tile(float* __restrict__ smem, const Fp8A
             p = __builtin_amdgcn_mfma_f32_16x16x32_f16(
                 halves(wv[d][m][f][i >> 1][2 * (i & 1)], wv[d][m][f][i >> 1][2 * (i & 1) + 1]), x[i], p, 0, 0, 0);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[m][f][h][q] = fmaf(p[q] * scale, sm, acc[m][f][h][q]);
+          for (int q = 0; q < 4; ++q) acc[m][f][h][q] = fmaf(__builtin_ldexpf(p[q], e), u, acc[m][f][h][q]);
           __builtin_amdgcn_sched_barrier(0);  // (few block sums at a time: registers)
         }
       }
