@@ -2,7 +2,7 @@
 
 Tolerances: an output of one product or copy is off by half a step of its type.  fp32 sums of n terms in any order are
 off by at most n half steps of the sum of the terms' magnitudes; the kernels add a thread's at most H / 16 terms, six
-steps of a wavefront and four wavefronts, or a token's k slots.
+steps of a wavefront and eight wavefronts, or a token's k slots.
 """
 
 import numpy as np
