@@ -855,7 +855,8 @@ moe_status check_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t E) {
 
 struct Fp8Plan {
   bool stream;
-  int max_tiles;  // row tiles, of the stream's height where it is one
+  int row_tiles;  // at most, of the stream's height where it is one
+  int max_tiles;  // with room for cut ones
   size_t flags, sched, sched_count, h, hq, hsc, total;
 };
 
@@ -904,8 +905,9 @@ Fp8Plan plan_fp8(const moe_shape& s, bool ffn) {
   Fp8Plan p{};
   const long long rows = (long long)s.num_tokens * s.top_k, H = s.hidden, I = s.intermediate;
   const int E = s.num_experts;
-  p.stream = rows > 0 && (ffn ? stream_fp8(s, 3 * H * I, (2 * H + I) / 3) : stream_fp8(s, H * I, I));
-  p.max_tiles = p.stream ? (int)stream_tiles(s) : (int)(rows / 256 + E + 1) + kUnits;  // (cut tiles)
+  p.stream = ffn ? stream_fp8(s, 3 * H * I, (2 * H + I) / 3) : stream_fp8(s, H * I, I);
+  p.row_tiles = (int)(p.stream ? stream_tiles(s) : rows / 256 + std::min<long long>(rows, E));
+  p.max_tiles = p.row_tiles + (p.stream ? 0 : kUnits);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at_ = o;
@@ -951,7 +953,7 @@ moe_status run_ffn_fp8(const moe_shape& s, const void* x, const float* xsc, cons
   if (p.stream) {
     float* h = at<float>(ws, p.h);
     up.out = h;
-    MOE_HIP(launch_stream_fp8(up, true, false, E, p.max_tiles, slots, true, st));
+    MOE_HIP(launch_stream_fp8(up, true, false, E, p.row_tiles, slots, true, st));
     // Quantised by the second product or by a launch, measured: FFN of 1 token over 128
     // experts of 2048 x 768 16.0 against 17.6 us, of 2 tokens 27.2 against 25.7; of 16 rows
     // over 8 experts of 1024 x 1024 14.6 against 16.1, of 8 of 2048 x 2048 17.7 against 19.5;
@@ -962,9 +964,8 @@ moe_status run_ffn_fp8(const moe_shape& s, const void* x, const float* xsc, cons
       down.A = reinterpret_cast<const uint8_t*>(h);
     } else {
       MOE_HIP(launch_quant_fp8(MOE_F32, h, slots, I, offsets + E, hq, hsc, st, flags));
-      down.sa_row = I / 128, down.sa_group = 1;
     }
-    MOE_HIP(launch_stream_fp8(down, false, fused, E, p.max_tiles, slots, false, st));
+    MOE_HIP(launch_stream_fp8(down, false, fused, E, p.row_tiles, slots, false, st));
     return MOE_OK;
   }
   const bool halves = few_tiles_fp8(s, H);
@@ -1782,7 +1783,7 @@ moe_status moe_grouped_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_
   if (p.stream) {
     // (an fp16 y adds to the flag word, which then has to be clear before)
     if (y_dtype == MOE_F16) MOE_HIP(launch_clear_flags(flags, st));
-    MOE_HIP(launch_stream_fp8(g, false, false, num_experts, p.max_tiles, rows, y_dtype != MOE_F16, st));
+    MOE_HIP(launch_stream_fp8(g, false, false, num_experts, p.row_tiles, rows, y_dtype != MOE_F16, st));
     return MOE_OK;
   }
   const bool halves = few_tiles_fp8(s, n);
