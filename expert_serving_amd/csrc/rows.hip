@@ -337,13 +337,23 @@ __global__ __launch_bounds__(NT) void k_slots(int T, int H, int k, const void* r
     }
   }
   if constexpr (DOT) {
+    // a step gives half of the lanes half of the slots each: KM + 5 - log2 KM exchanges in
+    // place of 6 KM (gradient of the combine of 64 x 2048 fp32, 8 slots: 7.3 -> 6.8 us), lane l ends with slot l / (64 / KM)
     __shared__ float s_dot[NT / 64][KM];
+    const int lane = threadIdx.x & 63;
+    int off = 32;
 #pragma unroll
-    for (int j = 0; j < KM; ++j) {
+    for (int half = KM / 2; half >= 1; half /= 2, off /= 2) {
+      const bool upper = lane & off;
 #pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) dot[j] += __shfl_xor(dot[j], off, 64);
-      if ((threadIdx.x & 63) == 0) s_dot[threadIdx.x >> 6][j] = dot[j];
+      for (int j = 0; j < half; ++j) {
+        const float keep = upper ? dot[j + half] : dot[j], give = upper ? dot[j] : dot[j + half];
+        dot[j] = keep + __shfl_xor(give, off, 64);
+      }
     }
+#pragma unroll
+    for (; off >= 1; off /= 2) dot[0] += __shfl_xor(dot[0], off, 64);
+    if (lane % (64 / KM) == 0) s_dot[threadIdx.x >> 6][lane / (64 / KM)] = dot[0];
     __syncthreads();
     if ((int)threadIdx.x < k) {
       float s = s_dot[0][threadIdx.x];
