@@ -876,8 +876,16 @@ struct Fp8Plan {
 // (112 MB) 24 against 20; of 60, 1 expert, 14336 x 4096 (112 MB) 31 against 33; of 700,
 // 32 experts, 1024 x 4096 (212 MB) 31 against 29; of 60, 1 expert, 28672 x 8192 (448 MB)
 // 109 against 85.
-bool stream_fp8(const moe_shape& s, long long matrix_bytes, long long mean_k) {
+//
+// Of any number of rows, streams take what their blocks (32 rows x 64 columns, of gate and
+// up 32) give no compute unit twice: the LDS tiles are then a few dozen
+// blocks.  Products of 1 expert: 100 rows x 4096 x 14336 (256 blocks) 47 against 82, 192 rows
+// (384) 90 against 87; 1024 rows x 512 x 7168 (256) 26 against 46, 512 x 1536 x 7168 (384) 49
+// against 47; 100 rows x 14336 x 4096 (896) 56 against 34; FFN of 100 rows, 2048 x 768 (128) 20
+// against 33.
+bool stream_fp8(const moe_shape& s, long long matrix_bytes, long long mean_k, long long strips) {
   const long long slots = (long long)s.num_tokens * s.top_k, E = s.num_experts;
+  if ((E == 1 ? (slots + 31) / 32 : stream_tiles(s)) * strips <= kComputeUnits) return true;
   if (slots / E >= 64) return false;
   return stream_tiles(s) * matrix_bytes <= mean_k * ((slots > 16 * E ? 40LL : 200LL) << 10);
 }
@@ -905,7 +913,8 @@ Fp8Plan plan_fp8(const moe_shape& s, bool ffn) {
   Fp8Plan p{};
   const long long rows = (long long)s.num_tokens * s.top_k, H = s.hidden, I = s.intermediate;
   const int E = s.num_experts;
-  p.stream = ffn ? stream_fp8(s, 3 * H * I, (2 * H + I) / 3) : stream_fp8(s, H * I, I);
+  p.stream = ffn ? stream_fp8(s, 3 * H * I, (2 * H + I) / 3, std::max(I / 32, (H + 63) / 64))
+                 : stream_fp8(s, H * I, I, (H + 63) / 64);
   p.row_tiles = (int)(p.stream ? stream_tiles(s) : rows / 256 + std::min<long long>(rows, E));
   p.max_tiles = p.row_tiles + (p.stream ? 0 : kUnits);
   size_t o = 0;

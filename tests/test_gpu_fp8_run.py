@@ -216,10 +216,49 @@ def test_ffn_of_many_tiles(counts, H, I):
     assert torch.equal(y, again)
 
 
+# 128 x 128 tiles and larger ones of every height, rows and columns that end inside a tile, and K from fewer stages than
+# are under way to more than share a load of scales
+TILES = [([200, 0, 31, 1, 300, 129], 1040), ([700], 1168), ([256, 257, 3, 64, 65, 33, 190, 130], 4112), ([450, 260], 5136)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("K", [128, 256, 384, 1152, 2304])
+@pytest.mark.parametrize("counts,N", TILES)
+def test_tiles(counts, N, K, dt):
+    say(f"fp8 tiles {counts} N={N} K={K} {dt}")
+    r = np.random.default_rng(N + K)
+    off = offsets_of(counts)
+    live, E = int(off[-1]), len(counts)
+    rows = live + 5
+    a, sa = P.exact_codes(r, rows, K), P.scales_of(r, rows, K // 128)
+    sa[live:] = np.nan
+    w, sw = P.exact_codes(r, E, N, K), P.scales_of(r, E, -(-N // 128), K // 128) / 64
+    y, flags = product(codes8(a), on(sa), on(off), codes8(w), on(sw), dt)
+    want, bound = P.product(a[:live], sa[:live], w, sw, off, True)
+    got = np64(y)
+    assert flags == 0 and np.all(np.abs(got[:live] - want) <= P.rounded(want, bound, dt))
+    assert (got[live:] == -7.0).all()
+
+
+@pytest.mark.parametrize("rows,N,K", [(700, 1152, 1280), (2600, 2560, 1280)])
+def test_tiles_of_all_codes_and_scales_far_apart(rows, N, K):
+    r = np.random.default_rng(rows)
+    a = P.e4m3(np.clip(r.normal(size=(rows, K)) * np.exp(1.5 * r.normal(size=(rows, K))) * 8, -448, 448))
+    w = P.e4m3(np.clip(r.normal(size=(1, N, K)) * 100, -448, 448))
+    sa = np.ldexp(1 + r.random((rows, K // 128)), r.integers(-120, -20, (rows, K // 128))).astype(np.float32)
+    sa[:, 3] = 0.0
+    sw = np.ldexp(1 + r.random((1, N // 128, K // 128)), r.integers(0, 20, (1, N // 128, K // 128))).astype(np.float32)
+    y, _ = product(codes8(a), on(sa), None, codes8(w), on(sw), "bf16")
+    want, bound = P.product(a, sa, w, sw, [0, rows], False)
+    # the scale of 0 may count as any up to 2^-126
+    low = 128 * 448.0 ** 2 * 2.0 ** -126 * sw[0, np.arange(N) // 128, 3].astype(np.float64)
+    assert np.all(np.abs(np64(y) - want) <= P.rounded(want, bound + low, "bf16"))
+
+
 # ---- values that are not finite --------------------------------------------------------------------------------
 
-# rows of one expert, N (or I), K: streams of 16 and of 32 rows, 128 x 128 tiles, large tiles
-PLANS = [(3, 128, 256), (29, 128, 1280), (300, 256, 256), (5000, 2560, 256)]
+# rows of one expert, N (or I), K: streams of 16 and of 32 rows and of more of them, 128 x 128 tiles, large tiles
+PLANS = [(3, 128, 256), (29, 128, 1280), (300, 256, 256), (700, 1152, 256), (5000, 2560, 256)]
 
 
 @pytest.mark.parametrize("rows,N,K", PLANS)
@@ -246,7 +285,8 @@ def test_products_of_values_that_are_not_finite(rows, N, K):
         assert torch.equal(y[~bad][:, 256:], base[~bad][:, 256:])
 
 
-@pytest.mark.parametrize("rows,I,H", [(3, 128, 256), (9, 4096, 128), (29, 128, 1280), (300, 256, 256), (5000, 1280, 256)])
+@pytest.mark.parametrize("rows,I,H", [(3, 128, 256), (9, 4096, 128), (29, 128, 1280), (300, 256, 256), (700, 640, 256),
+                                      (5000, 1280, 256), (3000, 256, 3328)])
 def test_ffn_of_values_that_are_not_finite(rows, I, H):
     """An h that is not finite, of a NaN scale or of an overflow, sets the flag and makes its own row NaN alone."""
     r = np.random.default_rng(rows)
@@ -265,7 +305,7 @@ def test_ffn_of_values_that_are_not_finite(rows, I, H):
         assert flags & abi.MOE_FLAG_H_RANGE and torch.isnan(y[bad]).all() and torch.equal(y[~bad], base[~bad]), (row, flags)
 
 
-@pytest.mark.parametrize("rows", [3, 29, 300])
+@pytest.mark.parametrize("rows", [3, 29, 300, 1500])
 def test_ffn_of_scales_far_apart(rows):
     """Row scales of 2^100 and 2^-100 against gate and up scales that bring them back: no step in between leaves the
     range of fp32."""
