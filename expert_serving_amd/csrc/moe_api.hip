@@ -890,8 +890,8 @@ bool stream_fp8(const moe_shape& s, long long matrix_bytes, long long mean_k, lo
   return stream_tiles(s) * matrix_bytes <= mean_k * ((slots > 16 * E ? 40LL : 200LL) << 10);
 }
 
-// A launch of single products on 128 x 128 tiles, two of a compute unit, instead of up to
-// 256 x 256 ones: where the estimated larger tiles (experts' last ones are short) would
+// A launch of single products (K = k) on 128 x 128 tiles, two of a compute unit, instead of
+// up to 256 x 256 ones: where the estimated larger tiles (experts' last ones are short) would
 // take less than half the compute units, or five eighths where experts have more than 128
 // rows, so that the larger tile is a tall one and a smaller tile halves its time.
 // Measured, 128 x 128 against 256 x 256: products of 1024 rows x 4096 x 4096 (64 tiles) 34
@@ -902,10 +902,19 @@ bool stream_fp8(const moe_shape& s, long long matrix_bytes, long long mean_k, lo
 // against 27; 600, 8 experts, 4096 x 4096 (128) 43 against 40, x 14336 164 against 133;
 // 400, 4 experts, 8192 x 8192 (128) 92 against 74.  The rule costs 256 rows x 28672 x 4096
 // (112), where a tile's weights serve twice the rows: 82 against 59.
-bool few_tiles_fp8(const moe_shape& s, int n) {
+// A short K ends in the epilogue early, and a second block of the compute unit goes on beside
+// it: the same up to 9 / 4 tiles per compute unit at K up to 1024, 5 / 4 up to 1536.  Products
+// of 5525 rows, 15 experts, 2688 (319 tiles) x 384 26 against 42, x 1536 47 against 54, x 4096 104
+// against 96; of 4096 rows x 4096 (272) x 1024 38 against 42, x 2048 56 against 55; of 2000 rows,
+// 20 experts, 3584 (280) x 1024 33 against 49; of 8192 rows, 8 experts, 4096 (576) x 1024 65 against
+// 72; of 1000 rows, 10 experts, 3584 (140) x 1536 28 against 27; of 16384, 8 experts, 4096 (1088)
+// x 1024 110 against 105; of 65536, 128 experts, 4096 x 768 460 against 370.
+bool few_tiles_fp8(const moe_shape& s, int n, int k) {
   const long long slots = (long long)s.num_tokens * s.top_k, E = s.num_experts;
   const long long tiles = std::max(slots / 256 + (E + 1) / 2, std::min(slots, E));
-  return tiles * ((n + 255) / 256) < (slots <= 128 * E ? kComputeUnits / 2 : kComputeUnits * 5 / 8);
+  const long long all = tiles * ((n + 255) / 256);
+  return all < (slots <= 128 * E ? kComputeUnits / 2 : kComputeUnits * 5 / 8) ||
+         (k <= 1024 && all <= kComputeUnits * 9 / 4) || (k <= 1536 && all <= kComputeUnits * 5 / 4);
 }
 
 // a batch of one slot per row of n columns and K = k, or (inter > 0) the FFN of a shape
@@ -977,7 +986,7 @@ moe_status run_ffn_fp8(const moe_shape& s, const void* x, const float* xsc, cons
     MOE_HIP(launch_stream_fp8(down, false, fused, E, p.row_tiles, slots, false, st));
     return MOE_OK;
   }
-  const bool halves = few_tiles_fp8(s, H);
+  const bool halves = few_tiles_fp8(s, H, I);
   MOE_HIP(launch_schedule_fp8(offsets, E, 0, sched, p.max_tiles, count, flags, halves ? 0 : (H + 255) / 256, st));
   MOE_HIP(launch_gemm_fp8(up, true, false, p.max_tiles, st));
   MOE_HIP(launch_gemm_fp8(down, false, halves, p.max_tiles, st));
@@ -1795,7 +1804,7 @@ moe_status moe_grouped_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_
     MOE_HIP(launch_stream_fp8(g, false, false, num_experts, p.row_tiles, rows, y_dtype != MOE_F16, st));
     return MOE_OK;
   }
-  const bool halves = few_tiles_fp8(s, n);
+  const bool halves = few_tiles_fp8(s, n, k);
   MOE_HIP(launch_schedule_fp8(expert_offsets, num_experts, rows, sched, p.max_tiles, count, flags,
                               halves ? 0 : (n + 255) / 256, st));
   MOE_HIP(launch_gemm_fp8(g, false, halves, p.max_tiles, st));
