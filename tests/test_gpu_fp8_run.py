@@ -182,7 +182,8 @@ def test_two_streams_at_once(T, H, I, E, k):
 MANY = [
     # rows per expert, N, K: more tiles than compute units, of every height, and a last round that is cut
     ([2048 + 17 * i for i in range(4)], 2560, 384), ([300, 5000, 1, 0, 700, 64, 129, 256], 1536, 256),
-    ([90, 200, 40, 300] * 16, 1040, 128), ([256 * 9 + 3], 8192, 128), ([64] * 128, 768, 256), ([1] * 200 + [3000], 512, 256),
+    ([256 * 48 + 100], 4096, 128), ([256 * 17], 4112, 1664), ([300, 2000, 1, 0, 700, 64, 129, 256], 4112, 1664),
+    ([190, 130, 70, 250] * 16, 1040, 1664), ([90, 200, 40, 300] * 16, 1040, 128), ([256 * 9 + 3], 8192, 128), ([64] * 128, 768, 256), ([1] * 200 + [3000], 512, 256),
 ]
 
 
@@ -240,7 +241,7 @@ def test_tiles(counts, N, K, dt):
     assert (got[live:] == -7.0).all()
 
 
-@pytest.mark.parametrize("rows,N,K", [(700, 1152, 1280), (2600, 2560, 1280)])
+@pytest.mark.parametrize("rows,N,K", [(700, 1152, 1280), (2600, 2560, 1280), (4500, 2560, 1664)])
 def test_tiles_of_all_codes_and_scales_far_apart(rows, N, K):
     r = np.random.default_rng(rows)
     a = P.e4m3(np.clip(r.normal(size=(rows, K)) * np.exp(1.5 * r.normal(size=(rows, K))) * 8, -448, 448))
@@ -258,7 +259,8 @@ def test_tiles_of_all_codes_and_scales_far_apart(rows, N, K):
 # ---- values that are not finite --------------------------------------------------------------------------------
 
 # rows of one expert, N (or I), K: streams of 16 and of 32 rows and of more of them, 128 x 128 tiles, large tiles
-PLANS = [(3, 128, 256), (29, 128, 1280), (300, 256, 256), (700, 1152, 256), (5000, 2560, 256)]
+PLANS = [(3, 128, 256), (29, 128, 1280), (300, 256, 256), (700, 1152, 256), (5000, 2560, 256),
+         (5000, 2560, 1664)]
 
 
 @pytest.mark.parametrize("rows,N,K", PLANS)
