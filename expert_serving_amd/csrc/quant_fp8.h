@@ -43,13 +43,14 @@ __device__ __forceinline__ float f8_quotient(float v, const F8Block& b) {
 }
 
 // The same for values that carry roundings of their own (h of an FFN), where the last
-// bit of the quotient decides nothing that they do not: one product.
+// bit of the quotient decides nothing that they do not: one product.  The powers of two
+// are f8_block's: the reciprocal instruction returns 0 for a maximum above 2^126.
 struct F8Near {
   float pre, factor;  // 448 / (amax * pre); 0 for a block of zeros
 };
 __device__ __forceinline__ F8Near f8_near(float amax) {
   F8Near r;
-  r.pre = amax < 1e-20f ? 0x1p60f : 1.0f;
+  r.pre = amax > 1e30f ? 0x1p-16f : (amax < 1e-20f ? 0x1p60f : 1.0f);
   const float x = amax * r.pre;
   r.factor = x > 0.f ? kFp8Max * __builtin_amdgcn_rcpf(x) : 0.f;
   return r;
