@@ -585,6 +585,8 @@ def quantize_fp8(t, stream=None):
 def quantize_fp8_weights(t, stream=None):
     """(codes float8_e4m3fn of t's shape, scales fp32 [..., ceil(N / 128), K / 128]) of weights [N, K] or [E, N, K]."""
     import torch
+    if t.dim() not in (2, 3):
+        raise ValueError("weights to quantise have to be [N, K] or [E, N, K]")
     dt, t = _to_quantise(t, stream)
     N, K = t.shape[-2:]
     experts = t.shape[0] if t.dim() == 3 else 1
