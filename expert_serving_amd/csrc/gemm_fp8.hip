@@ -534,7 +534,7 @@ hipError_t launch_schedule_fp8(const int32_t* offsets, int E, int static_rows, M
   return hipGetLastError();
 }
 
-hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, bool halves, int max_tiles, hipStream_t st) {
+hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, bool halves, int row_tiles, hipStream_t st) {
   static std::atomic<uint64_t> set_up{0}, set_down{0}, set_halves{0};
   constexpr int lds = max_of(tile_lds(128, 256), tile_lds(256, 256));  // (64 and 192 rows take less)
   constexpr int lds_halves = max_of(tile_lds(64, 128), tile_lds(128, 128));
@@ -542,7 +542,7 @@ hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, bool halves, int max_til
   if (dual) return launch_tiles(k_gemm_fp8<true>, lds, set_up, kUnits, a, (a.N + 127) / 128, st);
   if (!halves) return launch_tiles(k_gemm_fp8<false>, lds, set_down, kUnits, a, (a.N + 255) / 256, st);
   const int cols = (a.N + 127) / 128;
-  return launch_tiles(k_gemm_fp8_halves, lds_halves, set_halves, ((long long)max_tiles * 2 * cols + 7) / 8 * 8, a, cols, st);
+  return launch_tiles(k_gemm_fp8_halves, lds_halves, set_halves, ((long long)row_tiles * 2 * cols + 7) / 8 * 8, a, cols, st);
 }
 
 }  // namespace moe

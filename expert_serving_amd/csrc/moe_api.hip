@@ -856,7 +856,7 @@ moe_status check_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t E) {
 struct Fp8Plan {
   bool stream;
   int row_tiles;  // at most, of the stream's height where it is one
-  int max_tiles;  // with room for cut ones
+  int max_tiles;  // with room for cut ones, which launches of 128 x 128 tiles have none of
   size_t flags, sched, sched_count, h, hq, hsc, total;
 };
 
@@ -988,8 +988,8 @@ moe_status run_ffn_fp8(const moe_shape& s, const void* x, const float* xsc, cons
   }
   const bool halves = few_tiles_fp8(s, H, I);
   MOE_HIP(launch_schedule_fp8(offsets, E, 0, sched, p.max_tiles, count, flags, halves ? 0 : (H + 255) / 256, st));
-  MOE_HIP(launch_gemm_fp8(up, true, false, p.max_tiles, st));
-  MOE_HIP(launch_gemm_fp8(down, false, halves, p.max_tiles, st));
+  MOE_HIP(launch_gemm_fp8(up, true, false, p.row_tiles, st));
+  MOE_HIP(launch_gemm_fp8(down, false, halves, p.row_tiles, st));
   return MOE_OK;
 }
 
@@ -1807,7 +1807,7 @@ moe_status moe_grouped_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_
   const bool halves = few_tiles_fp8(s, n, k);
   MOE_HIP(launch_schedule_fp8(expert_offsets, num_experts, rows, sched, p.max_tiles, count, flags,
                               halves ? 0 : (n + 255) / 256, st));
-  MOE_HIP(launch_gemm_fp8(g, false, halves, p.max_tiles, st));
+  MOE_HIP(launch_gemm_fp8(g, false, halves, p.row_tiles, st));
   return MOE_OK;
 }
 

@@ -333,9 +333,10 @@ struct Fp8Args {
   const int32_t* offsets; // streams: [E + 1]; null: rows [0, static_rows) of expert 0
 };
 // one matrix: y; dual (gate/up): h as codes and scales.  Row tiles of up to 256 rows;
-// halves (one matrix): as two of up to 128, on 128 columns instead of 256.  A schedule
-// serves one launch of either kind.
-hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, bool halves, int max_tiles, hipStream_t st);
+// halves (one matrix): as two of up to 128, on 128 columns instead of 256, of at most
+// row_tiles uncut ones (the large tiles' blocks draw theirs from the schedule alone).  A
+// schedule serves one launch of either kind.
+hipError_t launch_gemm_fp8(const Fp8Args& a, bool dual, bool halves, int row_tiles, hipStream_t st);
 // count: all tiles, those before the quarter tiles, and a queue for each kind of launch
 constexpr int kFp8QueueUp = 4, kFp8QueueDown = 16, kFp8CountWords = 32;
 hipError_t launch_schedule_fp8(const int32_t* offsets, int E, int static_rows, MTile* sched, int max_tiles,
