@@ -23,7 +23,7 @@ def spread(counts, distinct):
 
 # rows per expert, H, I: a stream whose second product quantises h, streams with a launch for it, 128 x 128 tiles for
 # the second product, large tiles
-LIFTED = [([3], 256, 128), ([9], 128, 4096), ([29], 256, 1280), ([700], 256, 640), ([300] * 8, 4224, 1664)]
+LIFTED = [([3], 256, 128), ([9], 128, 4096), ([29], 256, 1280), ([700], 256, 640), ([300] * 8, 4224, 2304)]
 
 
 @pytest.mark.parametrize("counts,H,I", LIFTED)
