@@ -891,33 +891,39 @@ bool stream_fp8(const moe_shape& s, long long matrix_bytes, long long mean_k, lo
 }
 
 // A launch of single products (K = k) on 128 x 128 tiles, two of a compute unit, instead of
-// up to 256 x 256 ones: where the estimated larger tiles (experts' last ones are short) would
-// take less than half the compute units, or five eighths where experts have more than 128
-// rows, so that the larger tile is a tall one and a smaller tile halves its time.
-// Measured, 128 x 128 against 256 x 256: products of 1024 rows x 4096 x 4096 (64 tiles) 34
-// against 59 us, 2000 rows (128) 51 against 64, 2600 (160) 71 against 67; of 3000 rows, 16
-// experts, 2048 x 2048 (152) 28 against 39; of 1500 rows, 8 experts, 4096 x 14336 (144) 171
-// against 214; 1280 rows x 8192 x 8192 (160) 122 against 108.  Experts of at most 128 rows:
-// 700 rows, 4 experts, 4096 x 4096 (64) 32 against 48; 800, 8 experts, 3584 x 2048 (112) 24
-// against 27; 600, 8 experts, 4096 x 4096 (128) 43 against 40, x 14336 164 against 133;
-// 400, 4 experts, 8192 x 8192 (128) 92 against 74.  The rule costs 256 rows x 28672 x 4096
-// (112), where a tile's weights serve twice the rows: 82 against 59.
-// A short K ends in the epilogue early, and a second block of the compute unit goes on beside
-// it: the same up to 9 / 4 tiles per compute unit at K up to 1024, 5 / 4 up to 1536.  Products
-// of 5525 rows, 15 experts, 2688 (319 tiles) x 384 26 against 42, x 1536 47 against 54, x 4096 104
-// against 96; of 4096 rows x 4096 (272) x 1024 38 against 42, x 2048 56 against 55; of 2000 rows,
-// 20 experts, 3584 (280) x 1024 33 against 49; of 8192 rows, 8 experts, 4096 (576) x 1024 65 against
-// 72; of 1000 rows, 10 experts, 3584 (140) x 1536 28 against 27; of 16384, 8 experts, 4096 (1088)
-// x 1024 110 against 105; of 65536, 128 experts, 4096 x 768 460 against 370.
+// up to 256 x 256 ones.  A large tile reads half as much per multiplication, which a long
+// K repays as soon as they occupy most compute units: 128 x 128 where the estimated larger
+// tiles (experts' last ones are short) are at most 9 / 16 of the units, or less than half
+// where experts have at most 128 rows, so that the larger tile is no taller.  A short K ends
+// in the epilogue early, and a second block of the compute unit goes on beside it: the limit
+// is four tiles per unit at K up to 512, 11 / 4 up to 1024, 5 / 4 up to 1536, 9 / 8 up to 2048.
+// Measured, 128 x 128 against 256 x 256, estimated larger tiles in brackets.  K above 2048:
+// products of 1024 rows x 4096 (80) x 4096 34 against 59 us, 2000 rows (128) 49 against 65, 2600
+// (176) 75 against 68; of 1500 rows, 8 experts, 4096 (144) x 14336 174 against 208, of 4863 rows x
+// 1856 (152) x 14336 206 against 175.  Experts of at most 128 rows: of 700, 4 experts, 4096 (64) x
+// 4096 31 against 52; of 600, 8 experts, 4096 (128) x 14336 157 against 131, of 400, 4 experts, 8192
+// (128) x 8192 88 against 72, but 600, 8 experts, 4096 (128) x 4096 38 against 40.
+// K up to 2048: of 3000 rows, 16 experts, 2048 (152) 28 against 36, of 4096 rows x 4096 (272) 49
+// against 53, of 1470, 16 experts, 5568 (352) 55 against 51, of 561, 8 experts, 6848 (216) 38 against
+// 33.  Up to 1536: of 2588, 4 experts, 6592 (312) 44 against 52, of 1119, 16 experts, 6528 (416) 51
+// against 44.  Up to 1024: of 2000, 20 experts, 3584 (280) 32 against 46, of 8192, 8 experts, 4096
+// (576) 57 against 75, of 607, 16 experts, 9792 (624) 43 against 52, of 17607, 8 experts, 5376 (1512)
+// 148 against 133, of 65536, 128 experts, 4096 x 768 447 against 368.  Up to 512: of 5525, 15 experts,
+// 2688 (319) x 384 22 against 37, of 24105, 16 experts, 2112 (918) x 256 44 against 65, of 127, 64
+// experts, 6656 (1664) x 512 65 against 61.  The rule costs 256 rows x 28672 (224) x 4096, where every
+// weight serves one row tile on either side: 59 where 128 x 128 tiles take 44.
 bool few_tiles_fp8(const moe_shape& s, int n, int k) {
   const long long slots = (long long)s.num_tokens * s.top_k, E = s.num_experts;
   const long long tiles = std::max(slots / 256 + (E + 1) / 2, std::min(slots, E));
   const long long all = tiles * ((n + 255) / 256);
-  return all < (slots <= 128 * E ? kComputeUnits / 2 : kComputeUnits * 5 / 8) ||
-         (k <= 1024 && all <= kComputeUnits * 9 / 4) || (k <= 1536 && all <= kComputeUnits * 5 / 4);
+  if (k <= 512) return all <= kComputeUnits * 4;
+  if (k <= 1024) return all <= kComputeUnits * 11 / 4;
+  if (k <= 1536) return all <= kComputeUnits * 5 / 4;
+  if (k <= 2048) return all <= kComputeUnits * 9 / 8;
+  return slots <= 128 * E ? all < kComputeUnits / 2 : all <= kComputeUnits * 9 / 16;
 }
 
-// a batch of one slot per row of n columns and K = k, or (inter > 0) the FFN of a shape
+// a batch of one slot per row of n columns and K = k, or the FFN of a shape
 Fp8Plan plan_fp8(const moe_shape& s, bool ffn) {
   Fp8Plan p{};
   const long long rows = (long long)s.num_tokens * s.top_k, H = s.hidden, I = s.intermediate;
