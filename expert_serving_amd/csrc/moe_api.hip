@@ -896,7 +896,8 @@ bool stream_fp8(const moe_shape& s, long long matrix_bytes, long long mean_k, lo
 // tiles (experts' last ones are short) are at most 9 / 16 of the units, or less than half
 // where experts have at most 128 rows, so that the larger tile is no taller.  A short K ends
 // in the epilogue early, and a second block of the compute unit goes on beside it: the limit
-// is four tiles per unit at K up to 512, 11 / 4 up to 1024, 5 / 4 up to 1536, 9 / 8 up to 2048.
+// is four tiles per unit at K up to 512, 11 / 4 up to 1024, 5 / 4 up to 1536, 9 / 8 up to 2048
+// (but for experts of 65 to 128 rows, which fill one larger tile of that height).
 // Measured, 128 x 128 against 256 x 256, estimated larger tiles in brackets.  K above 2048:
 // products of 1024 rows x 4096 (80) x 4096 34 against 59 us, 2000 rows (128) 49 against 65, 2600
 // (176) 75 against 68; of 1500 rows, 8 experts, 4096 (144) x 14336 174 against 208, of 4863 rows x
@@ -904,13 +905,13 @@ bool stream_fp8(const moe_shape& s, long long matrix_bytes, long long mean_k, lo
 // 4096 31 against 52; of 600, 8 experts, 4096 (128) x 14336 157 against 131, of 400, 4 experts, 8192
 // (128) x 8192 88 against 72, but 600, 8 experts, 4096 (128) x 4096 38 against 40.
 // K up to 2048: of 3000 rows, 16 experts, 2048 (152) 28 against 36, of 4096 rows x 4096 (272) 49
-// against 53, of 1470, 16 experts, 5568 (352) 55 against 51, of 561, 8 experts, 6848 (216) 38 against
-// 33.  Up to 1536: of 2588, 4 experts, 6592 (312) 44 against 52, of 1119, 16 experts, 6528 (416) 51
-// against 44.  Up to 1024: of 2000, 20 experts, 3584 (280) 32 against 46, of 8192, 8 experts, 4096
-// (576) 57 against 75, of 607, 16 experts, 9792 (624) 43 against 52, of 17607, 8 experts, 5376 (1512)
-// 148 against 133, of 65536, 128 experts, 4096 x 768 447 against 368.  Up to 512: of 5525, 15 experts,
-// 2688 (319) x 384 22 against 37, of 24105, 16 experts, 2112 (918) x 256 44 against 65, of 127, 64
-// experts, 6656 (1664) x 512 65 against 61.  The rule costs 256 rows x 28672 (224) x 4096, where every
+// against 53, of 1470, 16 experts, 5568 (352) 55 against 51; of 561, 8 experts, 6848 (216) 38 against
+// 33, but of 347, 16 experts, 4096 (256) 33 against 37.  Up to 1536: of 2588, 4 experts, 6592 (312)
+// 44 against 52, of 1119, 16 experts, 6528 (416) 51 against 44.  Up to 1024: of 2000, 20 experts,
+// 3584 (280) 32 against 46, of 8192, 8 experts, 4096 (576) 57 against 75, of 607, 16 experts, 9792
+// (624) 43 against 52, of 17607, 8 experts, 5376 (1512) 148 against 133, of 65536, 128 experts, 4096
+// x 768 447 against 368.  Up to 512: of 5525, 15 experts, 2688 (319) x 384 22 against 37, of 24105,
+// 16 experts, 2112 (918) x 256 44 against 65, of 127, 64 experts, 6656 (1664) x 512 65 against 61.  The rule costs 256 rows x 28672 (224) x 4096, where every
 // weight serves one row tile on either side: 59 where 128 x 128 tiles take 44.
 bool few_tiles_fp8(const moe_shape& s, int n, int k) {
   const long long slots = (long long)s.num_tokens * s.top_k, E = s.num_experts;
@@ -919,7 +920,7 @@ bool few_tiles_fp8(const moe_shape& s, int n, int k) {
   if (k <= 512) return all <= kComputeUnits * 4;
   if (k <= 1024) return all <= kComputeUnits * 11 / 4;
   if (k <= 1536) return all <= kComputeUnits * 5 / 4;
-  if (k <= 2048) return all <= kComputeUnits * 9 / 8;
+  if (k <= 2048 && (slots <= 64 * E || slots > 128 * E)) return all <= kComputeUnits * 9 / 8;
   return slots <= 128 * E ? all < kComputeUnits / 2 : all <= kComputeUnits * 9 / 16;
 }
 
