@@ -862,32 +862,35 @@ struct Fp8Plan {
 
 // 8-bit floating-point products of fewer than 64 rows per expert stream their weights
 // (launch_stream_fp8) while the 32-row tiles together read at most 200 KB per k of their
-// (mean) K, or 40 KB where an expert has more than 16 rows and a step multiplies two
-// halves: the wavefronts of a stream share K and have too little of a short one, and a
-// second half costs a stream more than the LDS tiles.  Measured, streams against LDS
-// tiles: FFN of 1 token over 128 experts of 2048 x 768 (36 MB) 16 against 36 us, of 8
-// tokens (297 MB) 79 against 82, of 16 (594 MB) 120 against 107; of 2 tokens over 256
-// experts of 7168 x 2048 (672 MB) 137 against 144, of 4 (1386 MB) 268 against 255; of 8
-// tokens over 8 experts of 4096 x 14336 (1344 MB) 238 against 269, of 64 (2016 MB) 312
-// against 298; product of 128 rows, 8 experts, 4096 x 14336 (672 MB) 88 against 115; of
-// 300 rows, 64 experts, 1024 x 1024 (73 MB) 26 against 27, 128 experts (137 MB) 48
-// against 42.  More than 16 rows: of 300, 16 experts, 1024 x 1024 (25 MB) 9.1 against
-// 10.9, of 600, 32 experts (50 MB) 16.4 against 12.8; of 400, 16 experts, 2048 x 2048
-// (112 MB) 24 against 20; of 60, 1 expert, 14336 x 4096 (112 MB) 31 against 33; of 700,
-// 32 experts, 1024 x 4096 (212 MB) 31 against 29; of 60, 1 expert, 28672 x 8192 (448 MB)
-// 109 against 85.
+// (mean) K, 64 KB at a K of at most 1024, or where an expert has more than 16 rows 40 KB, 24
+// KB at a K of at most 2048 or more than 32 rows: the wavefronts of a stream share K and have
+// too little of a short one, a second half, which a step of more than 16 rows multiplies, costs
+// a stream more than the LDS tiles, and more than 32 rows read the weights again.  Measured,
+// streams against LDS tiles, in brackets those KB: FFN of 1 token over 128 experts of 2048 x
+// 768 (23) 16 against 29 us, of 8 tokens (188) 77 against 74, of 16 (375) 126 against 109; of 2 tokens over 256 experts of 7168 x 2048 (126) 132 against 140,
+// of 4 (260) 270 against 252; of 8 tokens over 8 experts of 4096 x 14336 (183) 212 against 234, of
+// 64 (275) 312 against 286; product of 128 rows, 8 experts, 4096 x 14336 (48) 92 against 115.  K
+// up to 1024: of 7 rows, 16 experts, 9024 x 256 (62) 8.0 against 10.0; of 37, 8 experts, 5504 x 1024
+// (48) 19.3 against 17.0; of 166, 16 experts, 4672 x 768 (96) 27 against 22; of 300, 64 experts, 1024
+// x 1024 (73) 26 against 21, 128 experts (137) 48 against 35.  More than 16 rows: of 171, 8
+// experts, 1152 x 512 (15) 6.8 against 8.4; of 211, 8 experts, 1152 x 2048 (16) 10.2 against 13.0; of
+// 1703, 64 experts, 256 x 1024 (29) 16.7 against 10.1; of 396, 8 experts, 1600 x 2048 (31) 19.2
+// against 13.7; of 192, 8 experts, 2624 x 4096 (36) 28.7 against 28.3; of 60, 1 expert, 14336 x 4096
+// (28) 31 against 21, 28672 x 8192 (56) 107 against 52; of 166, 8 experts, 3904 x 4096 (50) 29.5
+// against 31.9.
 //
 // Of any number of rows, streams take what their blocks (32 rows x 64 columns, of gate and
 // up 32) give no compute unit twice: the LDS tiles are then a few dozen
 // blocks.  Products of 1 expert: 100 rows x 4096 x 14336 (256 blocks) 47 against 82, 192 rows
-// (384) 90 against 87; 1024 rows x 512 x 7168 (256) 26 against 46, 512 x 1536 x 7168 (384) 49
-// against 47; 100 rows x 14336 x 4096 (896) 56 against 34; FFN of 100 rows, 2048 x 768 (128) 20
+// (384) 91 against 86; 1024 rows x 512 x 7168 (256) 26 against 46, 512 x 1536 x 7168 (384) 49
+// against 46; 100 rows x 14336 x 4096 (896) 56 against 30; FFN of 100 rows, 2048 x 768 (128) 20
 // against 33.
 bool stream_fp8(const moe_shape& s, long long matrix_bytes, long long mean_k, long long strips) {
   const long long slots = (long long)s.num_tokens * s.top_k, E = s.num_experts;
   if ((E == 1 ? (slots + 31) / 32 : stream_tiles(s)) * strips <= kComputeUnits) return true;
   if (slots / E >= 64) return false;
-  return stream_tiles(s) * matrix_bytes <= mean_k * ((slots > 16 * E ? 40LL : 200LL) << 10);
+  const long long kb = slots > 16 * E ? (mean_k > 2048 && slots <= 32 * E ? 40 : 24) : (mean_k > 1024 ? 200 : 64);
+  return stream_tiles(s) * matrix_bytes <= mean_k * (kb << 10);
 }
 
 // A launch of single products (K = k) on 128 x 128 tiles, two of a compute unit, instead of
