@@ -1003,8 +1003,16 @@ moe_status run_ffn_fp8(const moe_shape& s, const void* x, const float* xsc, cons
   return MOE_OK;
 }
 
-// The slots' rows of a call on token rows of a type, and the columns it can take.
-moe_status check_rows(const moe_shape& s, int dtype, const int32_t* row_of_slot, int32_t num_rows) {
+// A call on token rows of a type: the tokens, columns and slots of its shape, which say
+// nothing of the layer's types or weights here, and the columns it can take.
+moe_status check_rows(const moe_shape* shape, int dtype, const int32_t* row_of_slot, int32_t num_rows) {
+  if (!shape) return MOE_ERR_INVALID_ARG;
+  const moe_shape& s = *shape;
+  if (s.num_tokens < 0 || s.hidden <= 0 || s.top_k < 1) return MOE_ERR_INVALID_ARG;
+  if (s.top_k > kMaxTopK) return MOE_ERR_UNSUPPORTED;
+  if ((long long)s.num_tokens * s.top_k > (long long)INT_MAX / 2 ||
+      (long long)s.num_tokens * s.hidden > (long long)INT_MAX)
+    return MOE_ERR_UNSUPPORTED;
   if (!is_float_type(dtype) || num_rows < 0) return MOE_ERR_INVALID_ARG;
   if (s.hidden % (dtype == MOE_F32 ? 4 : 8)) return MOE_ERR_UNSUPPORTED;
   return need4(row_of_slot);
@@ -1849,8 +1857,7 @@ moe_status moe_grouped_ffn_fp8(const moe_shape* shape, const void* x_codes, cons
 
 moe_status moe_dispatch_rows(const moe_shape* shape, int32_t dtype, const void* x, const int32_t* row_of_slot,
                              const float* weights, int32_t num_rows, void* x_perm, void* stream) {
-  MOE_TRY(check_shape(shape));
-  MOE_TRY(check_rows(*shape, dtype, row_of_slot, num_rows));
+  MOE_TRY(check_rows(shape, dtype, row_of_slot, num_rows));
   MOE_TRY(need(x));
   MOE_TRY(opt4(weights));
   MOE_TRY(need(x_perm));
@@ -1862,8 +1869,7 @@ moe_status moe_dispatch_rows(const moe_shape* shape, int32_t dtype, const void* 
 
 moe_status moe_dispatch_rows_fp8(const moe_shape* shape, int32_t dtype, const void* x, const int32_t* row_of_slot,
                                  int32_t num_rows, void* x_codes, float* x_scales, void* stream) {
-  MOE_TRY(check_shape(shape));
-  MOE_TRY(check_rows(*shape, dtype, row_of_slot, num_rows));
+  MOE_TRY(check_rows(shape, dtype, row_of_slot, num_rows));
   if (shape->hidden % 128) return MOE_ERR_UNSUPPORTED;
   MOE_TRY(need(x));
   MOE_TRY(need(x_codes));
@@ -1877,8 +1883,7 @@ moe_status moe_dispatch_rows_fp8(const moe_shape* shape, int32_t dtype, const vo
 moe_status moe_dispatch_rows_backward(const moe_shape* shape, int32_t dtype, const void* d_perm,
                                       const int32_t* row_of_slot, int32_t num_rows, const float* weights,
                                       const void* x, void* d_x, float* d_weights, void* stream) {
-  MOE_TRY(check_shape(shape));
-  MOE_TRY(check_rows(*shape, dtype, row_of_slot, num_rows));
+  MOE_TRY(check_rows(shape, dtype, row_of_slot, num_rows));
   if (!d_x && !d_weights) return MOE_ERR_INVALID_ARG;
   MOE_TRY(need(d_perm));
   MOE_TRY(opt4(weights));
@@ -1897,9 +1902,8 @@ moe_status moe_dispatch_rows_backward(const moe_shape* shape, int32_t dtype, con
 moe_status moe_combine_backward(const moe_shape* shape, int32_t out_dtype, const void* d_out, int32_t y_dtype,
                                 const void* y_perm, const int32_t* row_of_slot, const float* topk_gates,
                                 int32_t num_rows, void* d_y, float* d_gates, void* stream) {
-  MOE_TRY(check_shape(shape));
   if (!is_float_type(out_dtype)) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_rows(*shape, y_dtype, row_of_slot, num_rows));
+  MOE_TRY(check_rows(shape, y_dtype, row_of_slot, num_rows));
   if (out_dtype != MOE_F32 && shape->hidden % 8) return MOE_ERR_UNSUPPORTED;
   if (!d_y && !d_gates) return MOE_ERR_INVALID_ARG;
   MOE_TRY(need(d_out));

@@ -567,8 +567,9 @@ moe_status moe_grouped_ffn_fp8(const moe_shape* shape, const void* x_codes, cons
                                void* y_perm, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- rows to expert order, and the gradients of dispatch and combine --------
- * For rows of any type (MOE_F32, MOE_BF16 or MOE_F16, whatever act_dtype is; H a
- * multiple of 8, of 4 when every row of the call is fp32) given the permutation
+ * For rows of any type (MOE_F32, MOE_BF16 or MOE_F16; H a multiple of 8, of 4 when
+ * every row of the call is fp32; num_tokens, hidden and top_k are all that these calls
+ * take from their shape, whose other fields may be anything) given the permutation
  * that moe_dispatch leaves in row_of_slot [T][top_k]; entries outside [0,
  * num_rows) are slots without a row, the others are distinct.  num_rows is the
  * rows that the permuted buffers hold.  Sums in fp32, in slot order, rounded once;

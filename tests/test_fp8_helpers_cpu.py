@@ -11,3 +11,42 @@ def test_weights_are_matrices(shape):
     """A tensor of other dimensions than [N, K] and [E, N, K] is refused rather than quantised in part."""
     with pytest.raises(ValueError, match="N, K"):
         abi.quantize_fp8_weights(torch.ones(shape))
+
+
+P = 0x10000   # aligned, never read
+
+
+@pytest.mark.parametrize("fields", [dict(act_dtype=abi.MOE_BF16), dict(act_dtype=abi.MOE_F32), dict(act_dtype=7),
+                                    dict(num_experts=0), dict(intermediate=0, score=9, out_dtype=5, num_groups=0)])
+def test_row_calls_take_tokens_columns_and_slots_from_their_shape(fields):
+    """H is a multiple of 8, or of 4 where every row is fp32, whatever the layer's types and weights are."""
+    L = abi.lib()
+
+    def calls(hidden, dt, out, top_k=2, T=5):
+        s = abi.make_shape(**dict(dict(num_tokens=T, hidden=hidden, num_experts=8, intermediate=64, top_k=top_k), **fields))
+        got = {L.moe_dispatch_rows(s, dt, P, P, P, 0, P, None)}
+        s.num_tokens = 0 if T > 0 else T           # (the gradients write without rows too)
+        return got | {L.moe_dispatch_rows_backward(s, dt, P, P, 0, P, P, P, P, None),
+                      L.moe_combine_backward(s, out, P, dt, P, P, P, 0, P, P, None)}
+
+    for hidden in (8, 40, 1000, 192):
+        for dt in (abi.MOE_F32, abi.MOE_BF16, abi.MOE_F16):
+            assert calls(hidden, dt, abi.MOE_F32) == {0}, (hidden, dt)
+    assert calls(12, abi.MOE_F32, abi.MOE_F32) == {0}
+    assert calls(12, abi.MOE_BF16, abi.MOE_BF16) == {abi.MOE_ERR_UNSUPPORTED}
+    assert calls(8, abi.MOE_F32, abi.MOE_F32, top_k=16) == {0}
+    assert calls(8, abi.MOE_F32, abi.MOE_F32, top_k=17) == {abi.MOE_ERR_UNSUPPORTED}
+    assert calls(8, abi.MOE_F32, abi.MOE_F32, top_k=0) == {abi.MOE_ERR_INVALID_ARG}
+    assert calls(0, abi.MOE_F32, abi.MOE_F32) == {abi.MOE_ERR_INVALID_ARG}
+    assert calls(8, abi.MOE_F32, abi.MOE_F32, T=-1) == {abi.MOE_ERR_INVALID_ARG}
+    s = abi.make_shape(**dict(dict(num_tokens=3, hidden=192, num_experts=8, intermediate=64, top_k=2), **fields))
+    assert L.moe_dispatch_rows_fp8(s, abi.MOE_BF16, P, P, 0, P, P, None) == abi.MOE_ERR_UNSUPPORTED
+    s.hidden = 384
+    assert L.moe_dispatch_rows_fp8(s, abi.MOE_BF16, P, P, 0, P, P, None) == 0
+
+
+def test_row_calls_refuse_more_elements_than_an_int_counts():
+    s = abi.make_shape(num_tokens=1 << 20, hidden=1 << 11, num_experts=8, intermediate=64, top_k=2)
+    assert abi.lib().moe_dispatch_rows(s, abi.MOE_BF16, P, P, P, 0, P, None) == abi.MOE_ERR_UNSUPPORTED
+    s.hidden, s.num_tokens, s.top_k = 8, 1 << 27, 16
+    assert abi.lib().moe_dispatch_rows(s, abi.MOE_BF16, P, P, P, 0, P, None) == abi.MOE_ERR_UNSUPPORTED
