@@ -1015,7 +1015,7 @@ moe_status check_rows(const moe_shape* shape, int dtype, const int32_t* row_of_s
     return MOE_ERR_UNSUPPORTED;
   if (!is_float_type(dtype) || num_rows < 0) return MOE_ERR_INVALID_ARG;
   if (s.hidden % (dtype == MOE_F32 ? 4 : 8)) return MOE_ERR_UNSUPPORTED;
-  return need4(row_of_slot);
+  return s.num_tokens > 0 ? need4(row_of_slot) : MOE_OK;
 }
 
 // ---- the layer, shared by the workspace and the no-allocation entry points ---
@@ -1764,10 +1764,10 @@ moe_status moe_quantize_fp8(int32_t rows, int32_t cols, int32_t src_dtype, const
                             float* scales, void* stream) {
   if (rows < 0 || cols <= 0 || !is_float_type(src_dtype)) return MOE_ERR_INVALID_ARG;
   if (cols % 128) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
   MOE_TRY(need(src));
   MOE_TRY(need(codes));
   MOE_TRY(need4(scales));
-  if (rows == 0) return MOE_OK;
   MOE_HIP(launch_quant_fp8(src_dtype, src, rows, cols, nullptr, codes, scales, static_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
@@ -1798,13 +1798,15 @@ moe_status moe_grouped_gemm_fp8(int32_t rows, int32_t n, int32_t k, int32_t num_
                                 void* stream) {
   MOE_TRY(check_gemm_fp8(rows, n, k, num_experts));
   if (!is_half_type(y_dtype)) return y_dtype == MOE_F32 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
-  MOE_TRY(need(a));
-  MOE_TRY(need4(a_scales));
+  if (rows > 0) {
+    MOE_TRY(need(a));
+    MOE_TRY(need4(a_scales));
+    MOE_TRY(need(y));
+  }
   if (!expert_offsets && num_experts != 1) return MOE_ERR_INVALID_ARG;
   MOE_TRY(opt4(expert_offsets));
   MOE_TRY(need(b));
   MOE_TRY(need4(b_scales));
-  MOE_TRY(need(y));
   MOE_TRY(need(ws));
   moe_shape s;
   const Fp8Plan p = plan_gemm_fp8(rows, n, k, num_experts, s);
@@ -1842,11 +1844,13 @@ moe_status moe_grouped_ffn_fp8(const moe_shape* shape, const void* x_codes, cons
   MOE_TRY(check_fp8_shape(shape));
   const moe_shape& s = *shape;
   if (!is_half_type(y_dtype)) return y_dtype == MOE_F32 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
-  MOE_TRY(need(x_codes));
-  MOE_TRY(need4(x_scales));
+  if (s.num_tokens > 0) {
+    MOE_TRY(need(x_codes));
+    MOE_TRY(need4(x_scales));
+    MOE_TRY(need(y_perm));
+  }
   MOE_TRY(need4(expert_offsets));
   MOE_TRY(check_fp8_ffn(experts));
-  MOE_TRY(need(y_perm));
   MOE_TRY(need(ws));
   const Fp8Plan p = plan_fp8(s, true);
   if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
@@ -1858,10 +1862,11 @@ moe_status moe_grouped_ffn_fp8(const moe_shape* shape, const void* x_codes, cons
 moe_status moe_dispatch_rows(const moe_shape* shape, int32_t dtype, const void* x, const int32_t* row_of_slot,
                              const float* weights, int32_t num_rows, void* x_perm, void* stream) {
   MOE_TRY(check_rows(shape, dtype, row_of_slot, num_rows));
+  if (shape->num_tokens == 0) return MOE_OK;
   MOE_TRY(need(x));
   MOE_TRY(opt4(weights));
+  if (num_rows == 0) return MOE_OK;
   MOE_TRY(need(x_perm));
-  if (shape->num_tokens == 0 || num_rows == 0) return MOE_OK;
   MOE_HIP(launch_dispatch_rows(*shape, dtype, x, row_of_slot, weights, num_rows, x_perm,
                                static_cast<hipStream_t>(stream)));
   return MOE_OK;
@@ -1871,10 +1876,11 @@ moe_status moe_dispatch_rows_fp8(const moe_shape* shape, int32_t dtype, const vo
                                  int32_t num_rows, void* x_codes, float* x_scales, void* stream) {
   MOE_TRY(check_rows(shape, dtype, row_of_slot, num_rows));
   if (shape->hidden % 128) return MOE_ERR_UNSUPPORTED;
+  if (shape->num_tokens == 0) return MOE_OK;
   MOE_TRY(need(x));
+  if (num_rows == 0) return MOE_OK;
   MOE_TRY(need(x_codes));
   MOE_TRY(need4(x_scales));
-  if (shape->num_tokens == 0 || num_rows == 0) return MOE_OK;
   MOE_HIP(launch_dispatch_rows_fp8(*shape, dtype, x, row_of_slot, num_rows, x_codes, x_scales,
                                    static_cast<hipStream_t>(stream)));
   return MOE_OK;
@@ -1884,8 +1890,9 @@ moe_status moe_dispatch_rows_backward(const moe_shape* shape, int32_t dtype, con
                                       const int32_t* row_of_slot, int32_t num_rows, const float* weights,
                                       const void* x, void* d_x, float* d_weights, void* stream) {
   MOE_TRY(check_rows(shape, dtype, row_of_slot, num_rows));
+  if (shape->num_tokens == 0) return MOE_OK;
   if (!d_x && !d_weights) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(need(d_perm));
+  if (num_rows > 0) MOE_TRY(need(d_perm));
   MOE_TRY(opt4(weights));
   if (d_weights) {
     if (!weights) return MOE_ERR_INVALID_ARG;
@@ -1893,7 +1900,6 @@ moe_status moe_dispatch_rows_backward(const moe_shape* shape, int32_t dtype, con
     MOE_TRY(need4(d_weights));
   }
   MOE_TRY(opt16(d_x));
-  if (shape->num_tokens == 0) return MOE_OK;
   MOE_HIP(launch_dispatch_rows_backward(*shape, dtype, d_perm, row_of_slot, num_rows, weights, x, d_x, d_weights,
                                         static_cast<hipStream_t>(stream)));
   return MOE_OK;
@@ -1905,13 +1911,17 @@ moe_status moe_combine_backward(const moe_shape* shape, int32_t out_dtype, const
   if (!is_float_type(out_dtype)) return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_rows(shape, y_dtype, row_of_slot, num_rows));
   if (out_dtype != MOE_F32 && shape->hidden % 8) return MOE_ERR_UNSUPPORTED;
-  if (!d_y && !d_gates) return MOE_ERR_INVALID_ARG;
+  if (shape->num_tokens == 0) return MOE_OK;
   MOE_TRY(need(d_out));
   MOE_TRY(need4(topk_gates));
-  MOE_TRY(opt16(d_y));
   MOE_TRY(opt4(d_gates));
-  if (d_gates) MOE_TRY(need(y_perm));
-  if (shape->num_tokens == 0) return MOE_OK;
+  if (num_rows > 0) {
+    if (!d_y && !d_gates) return MOE_ERR_INVALID_ARG;
+    MOE_TRY(opt16(d_y));
+    if (d_gates) MOE_TRY(need(y_perm));
+  } else if (!d_gates) {
+    return MOE_OK;
+  }
   MOE_HIP(launch_combine_backward(*shape, out_dtype, d_out, y_dtype, y_perm, row_of_slot, topk_gates, num_rows, d_y,
                                   d_gates, static_cast<hipStream_t>(stream)));
   return MOE_OK;

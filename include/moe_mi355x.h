@@ -515,6 +515,8 @@ moe_status moe_grouped_ffn_int8(const moe_shape* shape, const int8_t* x_codes, c
  * (fp16 2^-11, bf16 2^-8), so the products are written in those: y_dtype is
  * MOE_F16 or MOE_BF16, MOE_F32 is MOE_ERR_UNSUPPORTED.
  * Scales are not negative (the sign of one is unspecified in a product).
+ * The rows' buffers of a call with no rows may be NULL, here and in the row calls
+ * below.
  * A block with an infinity or NaN gets unspecified codes and a scale that is not
  * finite (NaN for a NaN); a row of a product with such a scale, or with a NaN
  * code, is NaN, as is a column of such a weight block.  A scale
@@ -572,7 +574,8 @@ moe_status moe_grouped_ffn_fp8(const moe_shape* shape, const void* x_codes, cons
  * take from their shape, whose other fields may be anything) given the permutation
  * that moe_dispatch leaves in row_of_slot [T][top_k]; entries outside [0,
  * num_rows) are slots without a row, the others are distinct.  num_rows is the
- * rows that the permuted buffers hold.  Sums in fp32, in slot order, rounded once;
+ * rows that the permuted buffers hold (0: they may be NULL; with no tokens every
+ * buffer may).  Sums in fp32, in slot order, rounded once;
  * no workspace. */
 
 /* x_perm[row_of_slot[t][j]] = weights[t][j] * x[t] (weights [T][top_k] fp32, NULL:

@@ -50,3 +50,31 @@ def test_row_calls_refuse_more_elements_than_an_int_counts():
     assert abi.lib().moe_dispatch_rows(s, abi.MOE_BF16, P, P, P, 0, P, None) == abi.MOE_ERR_UNSUPPORTED
     s.hidden, s.num_tokens, s.top_k = 8, 1 << 27, 16
     assert abi.lib().moe_dispatch_rows(s, abi.MOE_BF16, P, P, P, 0, P, None) == abi.MOE_ERR_UNSUPPORTED
+
+
+def test_buffers_without_rows_may_be_null():
+    """As those of torch tensors without elements are."""
+    L = abi.lib()
+    s = abi.make_shape(num_tokens=0, hidden=256, num_experts=8, intermediate=128, top_k=2)
+    some = abi.make_shape(num_tokens=3, hidden=256, num_experts=8, intermediate=128, top_k=2)
+    b, inv = abi.MOE_BF16, abi.MOE_ERR_INVALID_ARG
+    assert L.moe_quantize_fp8(0, 128, b, None, None, None, None) == 0
+    n = abi.moe_workspace_size_gemm_fp8(0, 64, 128, 4)
+    assert L.moe_grouped_gemm_fp8(0, 64, 128, 4, None, None, P, P, P, b, None, P, n, None) == 0
+    assert L.moe_grouped_gemm_fp8(0, 64, 128, 4, None, None, None, P, P, b, None, P, n, None) == inv
+    w = abi.MoeFp8Ffn(P, P, P, P, P, P)
+    assert L.moe_grouped_ffn_fp8(s, None, None, P, w, b, None, P, abi.moe_workspace_size_fp8(s), None) == 0
+    for rows in (0, 5):
+        assert L.moe_dispatch_rows(s, b, None, None, None, rows, None, None) == 0
+        assert L.moe_dispatch_rows_fp8(s, b, None, None, rows, None, None, None) == 0
+        assert L.moe_dispatch_rows_backward(s, b, None, None, rows, None, None, None, None, None) == 0
+        assert L.moe_combine_backward(s, b, None, b, None, None, None, rows, None, None, None) == 0
+    assert L.moe_dispatch_rows(some, b, P, P, None, 0, None, None) == 0
+    assert L.moe_dispatch_rows_fp8(some, b, P, P, 0, None, None, None) == 0
+    assert L.moe_combine_backward(some, b, P, b, None, P, P, 0, None, None, None) == 0
+    assert L.moe_dispatch_rows(some, b, P, P, None, 1, None, None) == inv
+    assert L.moe_dispatch_rows_fp8(some, b, P, P, 1, P, None, None) == inv
+    assert L.moe_dispatch_rows_backward(some, b, None, P, 1, None, None, P, None, None) == inv
+    assert L.moe_dispatch_rows_backward(some, b, P, P, 0, None, None, None, None, None) == inv
+    assert L.moe_combine_backward(some, b, P, b, None, P, P, 1, None, P, None) == inv
+    assert L.moe_combine_backward(some, b, P, b, P, P, P, 1, None, None, None) == inv

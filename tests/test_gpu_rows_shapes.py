@@ -33,3 +33,22 @@ def test_columns_that_a_bf16_layer_does_not_take(T, H, k, dropped, extra, dt):
         abi.moe_combine_backward(s, b, x, b, rows, ros, g, n, dy, dg)
         results.append((out, dx, dw, dy, dg))
     assert all(torch.equal(p, q) for p, q in zip(*results))
+
+
+def test_tensors_without_rows():
+    """A batch whose tokens all go elsewhere: the permuted tensors are empty ones."""
+    T, H, k, b = 5, 256, 2, abi.MOE_BF16
+    s = abi.make_shape(num_tokens=T, hidden=H, num_experts=16, intermediate=64, top_k=k)
+    ros, g = torch.full((T, k), -1, dtype=torch.int32, device=dev()), torch.ones(T, k, device=dev())
+    x = torch.ones(T, H, device=dev(), dtype=torch.bfloat16)
+    none, scales = torch.empty(0, H, device=dev(), dtype=torch.bfloat16), torch.empty(0, H // 128, device=dev())
+    codes = torch.empty(0, H, device=dev(), dtype=torch.uint8)
+    abi.moe_dispatch_rows(s, b, x, ros, g, 0, none)
+    abi.moe_dispatch_rows_fp8(s, b, x, ros, 0, codes, scales)
+    dx, dw, dg = torch.ones_like(x), torch.ones_like(g), torch.ones_like(g)
+    abi.moe_dispatch_rows_backward(s, b, none, ros, 0, g, x, dx, dw)
+    abi.moe_combine_backward(s, b, x, b, none, ros, g, 0, none, dg)
+    abi.moe_combine_backward(s, b, x, b, none, ros, g, 0, none, None)
+    assert (dx == 0).all() and (dw == 0).all() and (dg == 0).all()
+    c, v = abi.quantize_fp8(none)
+    assert c.shape == (0, H) and v.shape == (0, H // 128)
