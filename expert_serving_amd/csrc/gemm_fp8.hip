@@ -179,7 +179,7 @@ __device__ __forceinline__ void tile_fp8(uint8_t* smem, const Fp8Args& a, const 
   // since fragments start at multiples of 32 rows
   const int swz = (fr >> 1) & 7;
   const uint8_t* const fa = smem + (wm * WM + fr) * kStage;
-  const uint8_t* const fb = smem + (BM + (DUAL ? wn * WN : wn * WN) + fr) * kStage;
+  const uint8_t* const fb = smem + (BM + wn * WN + fr) * kStage;
   auto frag = [&](const uint8_t* row, int h) {
     return cat8(*reinterpret_cast<const u32x4*>(row + (((4 * h + fk) ^ swz) << 4)),
                 *reinterpret_cast<const u32x4*>(row + (((4 * h + 2 + fk) ^ swz) << 4)));

@@ -14,6 +14,7 @@
 // launch and one chain of loads.
 #include <type_traits>
 
+#include "half_bits.h"
 #include "moe_internal.h"
 #include "quant_fp8.h"
 
@@ -24,13 +25,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-  const uint32_t b = __float_as_uint(f);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return (b >> 16) | 0x40u;  // NaN stays NaN
-  return (b + (((b >> 16) & 1u) + 0x7FFFu)) >> 16;
-}
-__device__ __forceinline__ uint32_t f16_bits(float f) { return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f); }
 
 constexpr int type_bytes(int dt) { return dt == MOE_F32 ? 4 : 2; }
 

@@ -30,6 +30,7 @@
 // at 3.9 TB/s; of 128 rows, 8 experts, 4096 x 14336 88 us, 5.3 TB/s; of 1 row x 4096 x 4096
 // 8 us; FFN of 1 token over 128 experts of 2048 x 768 16 us for 38 MB, which is the
 // latency of two launches, a tile search, a chain of loads and a join each.
+#include "half_bits.h"
 #include "moe_internal.h"
 #include "quant_fp8.h"
 #include "swiglu.h"
@@ -46,13 +47,6 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 constexpr int kWaves = 8;
 constexpr int kStep = 128;  // codes of a step
 constexpr int kTileRows = 32;
-
-__device__ __forceinline__ uint32_t f16_bits(float f) { return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f); }
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-  const uint32_t b = __float_as_uint(f);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return (b >> 16) | 0x40u;  // NaN stays NaN
-  return (b + (((b >> 16) & 1u) + 0x7FFFu)) >> 16;
-}
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);

@@ -25,6 +25,7 @@
 // The row tiles are found in the kernel: every wavefront scans the experts'
 // offsets, one load and some thirty instructions, where a launch for a tile
 // list costs 3 us.
+#include "half_bits.h"
 #include "moe_internal.h"
 #include "quant_int8.h"
 #include "swiglu.h"
@@ -41,13 +42,6 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 constexpr int kWaves = 8;
 constexpr int kStep = 128;  // codes of a step
 constexpr int kTileRows = 32;
-
-__device__ __forceinline__ uint32_t f16_bits(float f) { return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f); }
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-  const uint32_t b = __float_as_uint(f);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return (b >> 16) | 0x40u;  // NaN stays NaN
-  return (b + (((b >> 16) & 1u) + 0x7FFFu)) >> 16;
-}
 
 struct StreamArgs {
   const uint8_t* A;          // codes, or fp16 rows (QUANT)
