@@ -8,7 +8,6 @@ functions, and a missing library raises instead of falling back.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -324,10 +323,14 @@ def moe_convert_bf16_to_f16(n, src, dst, stream=None):
 
 def _tensors_on(stream, device):
     """Context in which a helper makes the tensors of a call on `stream`: torch hands freed memory out again in the
-    order of the work of the stream it was allocated on, so memory of another stream could still be in use."""
-    if stream is None:
-        return contextlib.nullcontext()
+    order of the work of the stream it was allocated on, so memory of another stream could still be in use.  Without a
+    stream, the current one of the tensors' device, which need not be the current device.  The kernels cannot read a
+    host tensor: refused."""
     import torch
+    if device.type != "cuda":
+        raise ValueError("the tensor has to be on a GPU")
+    if stream is None:
+        return torch.cuda.device(device)
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device))
 
 

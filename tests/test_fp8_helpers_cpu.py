@@ -13,6 +13,20 @@ def test_weights_are_matrices(shape):
         abi.quantize_fp8_weights(torch.ones(shape))
 
 
+@pytest.mark.parametrize("f", [abi.quantize_fp8, abi.quantize_fp8_weights, abi.quantize_int8, abi.quantize_mxfp8,
+                               lambda t: abi.to_f16_weights(t.bfloat16())])
+def test_host_tensors_are_refused(f):
+    """A kernel that read one would fault."""
+    with pytest.raises(ValueError, match="GPU"):
+        f(torch.ones(128, 128))
+
+
+def test_helpers_run_on_their_tensors_device():
+    """Not on the current device, whose stream knows nothing of the other's work."""
+    at = abi._tensors_on(None, torch.device("cuda", 1))
+    assert isinstance(at, torch.cuda.device) and at.idx == 1
+
+
 P = 0x10000   # aligned, never read
 
 
