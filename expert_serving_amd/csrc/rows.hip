@@ -191,7 +191,7 @@ __global__ __launch_bounds__(256) void k_dispatch_rows_fp8(int items, int H, int
 }
 
 // The same on a matrix of whole blocks, in its own order: block b of 128 elements has
-// scale b.
+// scale b.  8192 x 14336 of bf16 59 us, 6.0 TB/s (two thirds of it reads).
 template <int DT>
 __global__ __launch_bounds__(256) void k_quant_fp8(long long items, int per_row, const int32_t* __restrict__ rows_dev,
                                                    const void* __restrict__ src, uint8_t* __restrict__ codes,
@@ -210,7 +210,8 @@ __global__ __launch_bounds__(256) void k_quant_fp8(long long items, int per_row,
 }
 
 // One block per 128 x 128 block of a weight matrix (fewer rows at its end); a thread
-// holds 64 values, 16 columns of four rows.  Done once per weight.
+// holds 64 values, 16 columns of four rows.  Done once per weight; bound by memory: 8 x
+// 14336 x 4096 of bf16 259 us, 5.4 TB/s, 128 x 768 x 2048 117 us, 1 x 4096 x 4096 11.5 us.
 template <int DT>
 __global__ __launch_bounds__(256) void k_quant_fp8_weights(int n, int k, const void* __restrict__ src,
                                                            uint8_t* __restrict__ codes, float* __restrict__ scales) {

@@ -43,7 +43,8 @@
  *     and set bits in a flag word at the head of the workspace.
  *   - Routing, counts, offsets and the permutation are bitwise deterministic;
  *     all other outputs are run-to-run deterministic (no atomics in sums).
- *   - num_tokens == 0 is valid and enqueues nothing.
+ *   - num_tokens == 0 is valid and enqueues nothing, as are no rows: outputs and the
+ *     flag word stay as they were.
  */
 #ifndef MOE_MI355X_H
 #define MOE_MI355X_H
@@ -562,7 +563,16 @@ typedef struct {
  * [T*top_k][H] and scales [T*top_k][H / 128]; h = silu(a) * u in fp32 is quantised
  * per row and block of 128 columns before the down projection (an h that is not
  * finite sets MOE_FLAG_H_RANGE, and its y row is NaN); y_perm in y_dtype (an fp16
- * value out of range sets MOE_FLAG_Y_RANGE).  Clears the workspace flag word. */
+ * value out of range sets MOE_FLAG_Y_RANGE).  Clears the workspace flag word.
+ * silu of a gate below -87.3, less than 1.1e-36 in magnitude, counts as 0.
+ * Few rows multiply the codes of gate and up as fp16 values and sum in fp32, more
+ * rows take the 8-bit units, whose sums are off by some 1e-5 (above), and the
+ * quotient 448 h / amax may be off by an fp32 rounding or two: an h that near to the
+ * middle between two codes can take either.  So the codes of a row's h, each half a step
+ * of its value from h either way, can differ with the number of rows of the call
+ * (2-norm error of y against exact sums 1.6e-3 with few rows of normal data, bf16's own
+ * rounding, and 1.9e-3 to 2.1e-3 with many); for the same call they are always
+ * the same. */
 moe_status moe_workspace_size_fp8(const moe_shape* shape, size_t* bytes);
 moe_status moe_grouped_ffn_fp8(const moe_shape* shape, const void* x_codes, const float* x_scales,
                                const int32_t* expert_offsets, const moe_fp8_ffn* experts, int32_t y_dtype,
