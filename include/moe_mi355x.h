@@ -570,7 +570,7 @@ typedef struct {
  * quotient 448 h / amax may be off by an fp32 rounding or two: an h that near to the
  * middle between two codes can take either.  So the codes of a row's h, each half a step
  * of its value from h either way, can differ with the number of rows of the call
- * (2-norm error of y against exact sums 1.6e-3 with few rows of normal data, bf16's own
+ * (2-norm error of y against exact sums 1.7e-3 with few rows of normal data, bf16's own
  * rounding, and 1.9e-3 to 2.1e-3 with many); for the same call they are always
  * the same. */
 moe_status moe_workspace_size_fp8(const moe_shape* shape, size_t* bytes);
