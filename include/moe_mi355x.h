@@ -35,16 +35,16 @@
  *     enqueues work; none synchronises with the host (except
  *     moe_read_device_flags), so calls can be captured in a graph.
  *   - Host-checkable errors return before anything is enqueued.
- *   - Every call that takes a workspace clears its flag word at the start;
- *     the word reports that call only.  A failed
+ *   - Every call that takes a workspace and enqueues work clears its flag word at the
+ *     start; the word reports that call only.  A failed
  *     launch returns MOE_ERR_HIP (the HIP error code is kept per thread, see
  *     moe_last_hip_error).  Errors found in data on the device (a k_t outside
  *     [1, k_max], an expert id outside [-1, E)) mark the affected slot unused
  *     and set bits in a flag word at the head of the workspace.
  *   - Routing, counts, offsets and the permutation are bitwise deterministic;
  *     all other outputs are run-to-run deterministic (no atomics in sums).
- *   - num_tokens == 0 is valid and enqueues nothing, as are no rows: outputs and the
- *     flag word stay as they were.
+ *   - num_tokens == 0 is valid and enqueues nothing, and so is rows == 0 where a call
+ *     takes its rows' number: outputs and the flag word stay as they were.
  */
 #ifndef MOE_MI355X_H
 #define MOE_MI355X_H
@@ -516,8 +516,7 @@ moe_status moe_grouped_ffn_int8(const moe_shape* shape, const int8_t* x_codes, c
  * (fp16 2^-11, bf16 2^-8), so the products are written in those: y_dtype is
  * MOE_F16 or MOE_BF16, MOE_F32 is MOE_ERR_UNSUPPORTED.
  * Scales are not negative (the sign of one is unspecified in a product).
- * The rows' buffers of a call with no rows may be NULL, here and in the row calls
- * below.
+ * The rows' buffers of a call with no rows may be NULL.
  * A block with an infinity or NaN gets unspecified codes and a scale that is not
  * finite (NaN for a NaN); a row of a product with such a scale, or with a NaN
  * code, is NaN, as is a column of such a weight block.  A scale
